@@ -315,6 +315,88 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
                           void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Token log-probabilities, entropies and top alternatives over a frozen LM head, and
+ * distillation from a teacher's top logits: what policy-gradient, preference and
+ * distillation losses, scoring and decoding need of the head, without the [M, V] logits.
+ * (The pages describe the head's cross-entropy only; these stand beside it.)  With hidden
+ * states X [M, D] (bf16), head W [V, D] (LORA_W_BF16 only, LORA_ERR_UNSUPPORTED otherwise)
+ * and scale = 1/temperature:
+ *
+ *     z = scale·X·Wᵀ        lse_m = log Σ_v exp(z_mv)        p_mv = exp(z_mv - lse_m)
+ *     logprob_mi = z_{m,ids_mi} - lse_m                      (n given tokens a row)
+ *     entropy_m  = -Σ_v p_mv·log p_mv
+ *     top k of a row: the k largest z, larger first, among equal ones the smaller id first
+ *
+ *     q_mi = softmax over i of scale·teacher_mi              (n listed tokens a row)
+ *     loss_m = Σ_i q_mi·(log q_mi - logprob_mi)              KL(teacher's list || student)
+ *
+ * and the gradient in X of upstream gradients c_mi of logprob_mi and g_m of entropy_m
+ * (distillation: c_mi = -dloss_m·q_mi, g_m = 0):
+ *
+ *     dz_mv = Σ_{i: ids_mi = v} c_mi - p_mv·(Σ_i c_mi + g_m·(log p_mv + entropy_m))
+ *     dX = scale·dz·W
+ *
+ * W is frozen: there is no dW.  The loss is not multiplied by temperature².
+ *
+ * Entries with ids_mi == ignore_index have logprob 0, no weight in q and no gradient
+ * (ignore_index may be a valid id, which is then never counted); a row without any other has
+ * loss 0 and a zero gradient, and so has a row whose listed teacher logits are all -inf.  An
+ * id outside [0, V) that is not ignore_index gives a NaN logprob, and a NaN loss where its q is
+ * not 0 (its gradient is unspecified).  An id listed twice counts twice.  A NaN or +inf
+ * teacher logit gives that row a NaN loss.  Rows whose logits are not finite give NaN.
+ *
+ * lora_logprob_fwd: ids device int32 [M, n], 0 <= n <= 128 (n = 0: ids and logprob unused);
+ * logprob fp32 [M, n], entropy fp32 [M] (or NULL), lse fp32 [M]; 0 <= k <= 32 and k <= V,
+ * top_ids int32 [M, k] and top_logprob fp32 [M, k] (unused for k = 0; should a row have fewer
+ * than k logits that are not NaN, id -1 and NaN fill up).  lora_distill_fwd: 1 <= n <= 128,
+ * teacher_logits fp32 [M, n] (log-probabilities will do: lora_logprob_fwd's top_ids and
+ * top_logprob on the teacher's head are a list), loss fp32 [M].  All device, all out but X,
+ * W, ids and teacher_logits.  Up to 128 rows run on a kernel that reads the head once for all
+ * of them.
+ *
+ * saved: NULL, or device memory of lora_head_saved_bytes(M, V) in which the forward keeps
+ * exp(z - tile maximum) in fp16 (2·M·V bytes and a little) for the backward, which then skips
+ * the logits' product, a third of the training step's work.  The backward turns the buffer
+ * into dz in place: it serves one backward.  With saved == NULL the backward recomputes the
+ * logits: over the whole vocabulary at once if the workspace holds dz [M, V], else slice by
+ * slice, as lora_ce_bwd.
+ *
+ * Backward: ids, n, ignore_index, scale, X and W as in the forward, lse (and, with dentropy,
+ * entropy) from it; dlogprob fp32 [M, n] or NULL, dentropy fp32 [M] or NULL (NULL: zero);
+ * dloss fp32 [M]; dX bf16 [M, D] (out).
+ *
+ * Workspace: lora_head_fwd_workspace_bytes(M, D, V, n, k) for the forward (k = 0 for
+ * lora_distill_fwd); lora_head_bwd_workspace_bytes(M, D, V, n, slice) for the backward, slice
+ * = 0 with a saved forward, else the vocabulary rows a slice (V or more: all at once; fewer
+ * than 256 columns' room is LORA_ERR_WORKSPACE).  One buffer may serve both; its first 256
+ * bytes must be zero before its first use.  Limits as for the layer: D % 8 == 0, V % 8 == 0;
+ * scale finite and > 0; M == 0 enqueues nothing.
+ */
+size_t lora_head_fwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n, int32_t k);
+size_t lora_head_bwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n, int64_t slice);
+size_t lora_head_saved_bytes(int64_t M, int64_t V);
+
+lora_status_t lora_logprob_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,
+                               int32_t ignore_index, float scale, int32_t k, float* logprob, float* entropy,
+                               float* lse, int32_t* top_ids, float* top_logprob, void* saved,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+lora_status_t lora_logprob_bwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,
+                               int32_t ignore_index, float scale, const float* lse, const float* entropy,
+                               const float* dlogprob, const float* dentropy, void* saved, void* dX,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+lora_status_t lora_distill_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids,
+                               const float* teacher_logits, int32_t n, int32_t ignore_index, float scale,
+                               float* loss, float* lse, void* saved,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+lora_status_t lora_distill_bwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids,
+                               const float* teacher_logits, int32_t n, int32_t ignore_index, float scale,
+                               const float* lse, const float* dloss, void* saved, void* dX,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Standalone dequantization of a weight of any format to bf16 [N,K] (device, out),
  * element by element as defined for lora_weight_t (bit-exact; a bf16 weight is copied).
  * W_out must not overlap the weight's arrays.

@@ -31,4 +31,7 @@ from .lora_oracle import (  # noqa: F401
     quantize_rowwise8,
     cross_entropy,
     cross_entropy_rows_bits,
+    token_logprobs,
+    teacher_softmax,
+    distill,
 )

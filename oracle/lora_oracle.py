@@ -481,3 +481,75 @@ def cross_entropy_rows_bits(X_rows_bits: np.ndarray, W_bits: np.ndarray, labels:
         for v0 in range(0, V, chunk):
             dX += P[:, v0:v0 + chunk] @ bf16_to_f64(W_bits[v0:v0 + chunk])
     return loss, lse, dX
+
+
+# ----------------------------------------------------------------------------
+# token log-probabilities, entropy, alternatives and distillation over a frozen LM head
+# ----------------------------------------------------------------------------
+
+
+def _head_logits(X, W, temperature):
+    return (np.asarray(X, dtype=np.float64) @ np.asarray(W, dtype=np.float64).T) / float(temperature)
+
+
+def _log_softmax(z):
+    zmax = z.max(axis=1, keepdims=True)
+    return (z - zmax) - np.log(np.sum(np.exp(z - zmax), axis=1, keepdims=True))
+
+
+def token_logprobs(X, W, ids, ignore_index: int, temperature: float = 1.0, k: int = 0, dlogprob=None, dentropy=None):
+    """Plain definitions on the full logits ``z = X·Wᵀ/temperature``: log-probabilities of
+    ``ids [M, n]`` (0 for entries equal to ``ignore_index``, NaN outside ``[0, V)``), entropies
+    ``-Σ p·log p``, the ``k`` largest logits' ids (smaller id first among equal ones) and
+    log-probabilities, and, given upstream gradients, dX by the chain rule through the softmax's
+    Jacobian: ``dz = dl - p·Σ dl`` for the gradient ``dl`` of all log-probabilities, where the
+    entropy adds ``-dentropy·p·(log p + 1)`` to ``dl``.  Returns a dict."""
+    z = _head_logits(X, W, temperature)
+    logp = _log_softmax(z)
+    p = np.exp(logp)
+    M, V = z.shape
+    ids = np.asarray(ids, dtype=np.int64).reshape(M, -1)
+    keep = ids != ignore_index
+    inside = keep & (ids >= 0) & (ids < V)
+    rows = np.arange(M)[:, None]
+    lp = np.where(inside, logp[rows, np.where(inside, ids, 0)], np.where(keep, np.nan, 0.0))
+    order = np.argsort(-z, axis=1, kind="stable")[:, :k]
+    out = {"z": z, "logprob": lp, "entropy": -np.sum(p * logp, axis=1), "top_ids": order,
+           "top_logprob": np.take_along_axis(logp, order, axis=1)}
+    if dlogprob is not None or dentropy is not None:
+        dl = np.zeros_like(z)
+        if dlogprob is not None:
+            np.add.at(dl, (np.broadcast_to(rows, ids.shape)[inside], ids[inside]),
+                      np.asarray(dlogprob, dtype=np.float64).reshape(M, -1)[inside])
+        if dentropy is not None:
+            dl -= np.asarray(dentropy, dtype=np.float64)[:, None] * p * (logp + 1.0)
+        dz = dl - p * dl.sum(axis=1, keepdims=True)
+        out["dz"] = dz / float(temperature)
+        out["dX"] = out["dz"] @ np.asarray(W, dtype=np.float64)
+    return out
+
+
+def teacher_softmax(ids, teacher_logits, ignore_index: int, temperature: float = 1.0):
+    """q ``[M, n]``: the softmax over a row's listed teacher logits, entries with
+    ``ignore_index`` left out; a row without any, or with only -inf, is all zero."""
+    t = np.where(np.asarray(ids) != ignore_index, np.asarray(teacher_logits, dtype=np.float64) / float(temperature),
+                 -np.inf)
+    q = np.zeros_like(t)
+    for m in range(t.shape[0]):
+        if np.any(t[m] > -np.inf):
+            e = np.exp(t[m] - t[m].max())
+            q[m] = e / e.sum()
+    return q
+
+
+def distill(X, W, ids, teacher_logits, ignore_index: int, temperature: float = 1.0, dloss=None):
+    """``loss_m = Σ_i q_mi·(log q_mi - log p_{m,ids_mi})`` with q from :func:`teacher_softmax` and
+    p the softmax of ``X·Wᵀ/temperature`` (terms with q = 0 are 0), and dX of ``Σ dloss·loss``:
+    the gradient of log-probabilities with ``dlogprob = -dloss·q``.  Returns a dict."""
+    q = teacher_softmax(ids, teacher_logits, ignore_index, temperature)
+    dl = None if dloss is None else -np.asarray(dloss, dtype=np.float64)[:, None] * q
+    out = token_logprobs(X, W, ids, ignore_index, temperature, 0, dl)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        out["loss"] = np.where(q > 0, q * (np.log(q) - out["logprob"]), 0.0).sum(axis=1)
+    out["q"] = q
+    return out

@@ -44,7 +44,12 @@ EXPORTED = (
     "lora_ce_workspace_bytes", "lora_ce_fwd", "lora_ce_bwd",
     "lora_linear_bwd_ex", "lora_grouped_bwd_ex", "lora_mlp_bwd_ex", "lora_round_bf16",
     "lora_testing_tcproj_extra_tile", "lora_testing_tcproj_splits",
+    "lora_head_fwd_workspace_bytes", "lora_head_bwd_workspace_bytes", "lora_head_saved_bytes",
+    "lora_logprob_fwd", "lora_logprob_bwd", "lora_distill_fwd", "lora_distill_bwd",
 )
+
+LORA_HEAD_MAX_IDS = 128  # given tokens (or teacher entries) a row
+LORA_HEAD_MAX_TOP = 32   # alternatives a row
 
 LORA_MAX_SEGMENTS = 8
 
@@ -125,6 +130,20 @@ def _load() -> ctypes.CDLL:
     lib.lora_ce_fwd.restype = i32
     lib.lora_ce_bwd.argtypes = [vp, i64, W, vp, i32, vp, vp, vp, vp, sz, vp]
     lib.lora_ce_bwd.restype = i32
+    lib.lora_head_fwd_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    lib.lora_head_fwd_workspace_bytes.restype = sz
+    lib.lora_head_bwd_workspace_bytes.argtypes = [i64, i64, i64, i32, i64]
+    lib.lora_head_bwd_workspace_bytes.restype = sz
+    lib.lora_head_saved_bytes.argtypes = [i64, i64]
+    lib.lora_head_saved_bytes.restype = sz
+    lib.lora_logprob_fwd.argtypes = [vp, i64, W, vp, i32, i32, f32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.lora_logprob_fwd.restype = i32
+    lib.lora_logprob_bwd.argtypes = [vp, i64, W, vp, i32, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.lora_logprob_bwd.restype = i32
+    lib.lora_distill_fwd.argtypes = [vp, i64, W, vp, vp, i32, i32, f32, vp, vp, vp, vp, sz, vp]
+    lib.lora_distill_fwd.restype = i32
+    lib.lora_distill_bwd.argtypes = [vp, i64, W, vp, vp, i32, i32, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.lora_distill_bwd.restype = i32
     lib.lora_merge.argtypes = [W, vp, vp, i32, f32, vp, vp]
     lib.lora_merge.restype = i32
     lib.lora_device_status.argtypes = [vp, vp]
@@ -460,3 +479,55 @@ def lora_ce_bwd(X, M: int, W: LoraWeight, labels, ignore_index: int, lse, dloss,
     nb = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
     _check(_lib.lora_ce_bwd(_ptr(X), int(M), ctypes.byref(w), _ptr(labels), int(ignore_index), _ptr(lse),
                             _ptr(dloss), _ptr(dX), _ptr(workspace), int(nb), _stream(stream)), "lora_ce_bwd")
+
+
+def head_fwd_workspace_bytes(M: int, D: int, V: int, n: int, k: int = 0) -> int:
+    return int(_lib.lora_head_fwd_workspace_bytes(int(M), int(D), int(V), int(n), int(k)))
+
+
+def head_bwd_workspace_bytes(M: int, D: int, V: int, n: int, slice_: int = 0) -> int:
+    return int(_lib.lora_head_bwd_workspace_bytes(int(M), int(D), int(V), int(n), int(slice_)))
+
+
+def head_saved_bytes(M: int, V: int) -> int:
+    return int(_lib.lora_head_saved_bytes(int(M), int(V)))
+
+
+def lora_logprob_fwd(X, M: int, W: LoraWeight, ids, n: int, ignore_index: int, scale: float, k: int, logprob, entropy,
+                     lse, top_ids, top_logprob, saved, workspace, ws_bytes=None, stream=None) -> None:
+    """Log-probabilities of given tokens, entropy and top alternatives of X·Wᵀ (see lora_linear.h)."""
+    w = W.c_struct()
+    nb = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.lora_logprob_fwd(_ptr(X), int(M), ctypes.byref(w), _ptr(ids), int(n), int(ignore_index), float(scale),
+                                 int(k), _ptr(logprob), _ptr(entropy), _ptr(lse), _ptr(top_ids), _ptr(top_logprob),
+                                 _ptr(saved), _ptr(workspace), int(nb), _stream(stream)), "lora_logprob_fwd")
+
+
+def lora_logprob_bwd(X, M: int, W: LoraWeight, ids, n: int, ignore_index: int, scale: float, lse, entropy, dlogprob,
+                     dentropy, saved, dX, workspace, ws_bytes=None, stream=None) -> None:
+    """Gradient in X of upstream gradients of the log-probabilities and the entropy."""
+    w = W.c_struct()
+    nb = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.lora_logprob_bwd(_ptr(X), int(M), ctypes.byref(w), _ptr(ids), int(n), int(ignore_index), float(scale),
+                                 _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy), _ptr(saved), _ptr(dX),
+                                 _ptr(workspace), int(nb), _stream(stream)), "lora_logprob_bwd")
+
+
+def lora_distill_fwd(X, M: int, W: LoraWeight, ids, teacher_logits, n: int, ignore_index: int, scale: float, loss, lse,
+                     saved, workspace, ws_bytes=None, stream=None) -> None:
+    """KL of a teacher's listed logits against X·Wᵀ, per row (see lora_linear.h)."""
+    w = W.c_struct()
+    nb = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.lora_distill_fwd(_ptr(X), int(M), ctypes.byref(w), _ptr(ids), _ptr(teacher_logits), int(n),
+                                 int(ignore_index), float(scale), _ptr(loss), _ptr(lse), _ptr(saved), _ptr(workspace),
+                                 int(nb), _stream(stream)), "lora_distill_fwd")
+
+
+def lora_distill_bwd(X, M: int, W: LoraWeight, ids, teacher_logits, n: int, ignore_index: int, scale: float, lse,
+                     dloss, saved, dX, workspace, ws_bytes=None, stream=None) -> None:
+    """Gradient of Σ dloss·loss in X."""
+    w = W.c_struct()
+    nb = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.lora_distill_bwd(_ptr(X), int(M), ctypes.byref(w), _ptr(ids), _ptr(teacher_logits), int(n),
+                                 int(ignore_index), float(scale), _ptr(lse), _ptr(dloss), _ptr(saved), _ptr(dX),
+                                 _ptr(workspace), int(nb), _stream(stream)), "lora_distill_bwd")

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "liblora_linear.so")
 LIB_CHECKED = os.path.join(PKG, "liblora_linear_checked.so")
 SOURCES = ["lora_api.cu"]
 HEADERS = ["ptx.cuh", "dequant.cuh", "gemm_common.cuh", "gemm_pair.cuh", "gemm_q.cuh", "skinny.cuh", "dualproj.cuh",
-           "elementwise.cuh", "streamk.cuh", "tcproj.cuh"]
+           "elementwise.cuh", "streamk.cuh", "tcproj.cuh", "head.cuh", "head_rows.cuh"]
 
 
 def nvcc_path() -> str:

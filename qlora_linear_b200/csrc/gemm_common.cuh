@@ -6,6 +6,21 @@
 
 namespace lora {
 
+// Per-row work over an LM head (head.cuh): logits z = scale·(the GEMM's output columns).
+struct HeadArgs {
+  float scale;
+  int n;                     // given tokens a row
+  const int2* sorted;        // [M][n] by id: (id, position) forward, (id, coefficient) backward
+  float* id_logit;           // forward: [M][n]
+  int k, kp;                 // alternatives a row, and the power of two >= k of their groups
+  unsigned* bound;           // forward: [M][kp] group maxima over the tiles seen so far
+  unsigned long long* cand;  // forward: [M][tiles][k] candidate keys
+  float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, candidates)
+  __half* expz;              // [M][V] e^{z - tile max}, or null
+  float* tile_max;           // [M][tiles], with expz
+  const float4* rowp;        // backward: [M] (lse, Σc + g_H·H, g_H, -)
+};
+
 struct PairParams {
   int M;               // rows of Aop / out
   int Nout;            // columns of out
@@ -35,6 +50,7 @@ struct PairParams {
   const float* lse;        // EPI_CE_DLOGITS: [M]
   const float* dloss;      // EPI_CE_DLOGITS: [M] upstream gradient of each row's loss
   float* acc32;            // EPI_ACC_F32: [M, Nout] fp32 running sum
+  HeadArgs head;           // EPI_HEAD_FWD, EPI_HEAD_DLOGITS (v0 as above)
   int acc_mode;            // EPI_ACC_F32: bit 0 add the running sum, bit 1 write bf16 to out instead
   __nv_bfloat16* out;  // [M, Nout] row-major
   // Stream-K schedule (EPI_STORE only, see UnitWalk): sk_on != 0 runs the first
@@ -64,6 +80,9 @@ enum : int {
                        // label's logit; no logits are written
   EPI_CE_DLOGITS = 4,  // accumulator = logits: out <- dloss·(exp(z - lse) - [label == column])
   EPI_ACC_F32 = 5,     // out/acc32 <- accumulator (+ acc32), see acc_mode
+  EPI_HEAD_FWD = 6,    // accumulator = logits / scale: per row and tile the sums, given tokens'
+                       // logits and candidates of head.cuh; out is not written
+  EPI_HEAD_DLOGITS = 7,  // accumulator = logits / scale: out <- scale·dz (head.cuh)
 };
 
 template <int EPI>

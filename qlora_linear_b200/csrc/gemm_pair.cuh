@@ -33,6 +33,7 @@
 #pragma once
 
 #include "gemm_common.cuh"
+#include "head.cuh"
 
 namespace lora {
 
@@ -59,6 +60,13 @@ struct PairCfg {
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 8 * NUM_BARS + 16;
   static_assert(STAGE_BYTES % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
+  // The head's forward keeps each thread's best keys behind the barriers (8-byte slots).
+  static constexpr int LIST_OFF = STAGES * STAGE_BYTES + 8 * NUM_BARS + 16;
+  template <int EPI>
+  static constexpr int smem_bytes() {
+    return EPI == EPI_HEAD_FWD ? SMEM_BYTES + kHeadMaxTop * kHeadListThreads * 8 : SMEM_BYTES;
+  }
+  static_assert(LIST_OFF % 8 == 0 && SMEM_BYTES + kHeadMaxTop * kHeadListThreads * 8 <= 232448, "shared memory");
 };
 
 template <bool B_MN, int EPI>
@@ -255,9 +263,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
     while (w.next(un)) {
       int mb, nb;
       pair_tile_coords(un.t, num_m, num_n, p.group_m, mb, nb);
+      const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
+      int first_id = 0;
+      if constexpr (EPI == EPI_HEAD_FWD) {  // found while the accumulator fills
+        if (row < p.M && p.head.n > 0)
+          first_id = head_first_id(p.head.sorted + static_cast<size_t>(row) * p.head.n, p.head.n, nb * C::BN);
+      }
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, wc)) break;
       tc_fence_after();
-      const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * C::BN);
       if constexpr (EPI == EPI_SWIGLU_FWD) {
@@ -360,6 +373,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
             }
           }
         }
+      } else if constexpr (EPI == EPI_HEAD_FWD) {
+        auto* lists = reinterpret_cast<unsigned long long*>(smem + C::LIST_OFF);
+        head_fwd_tile(p.head, tbase, min(C::BN, p.Nout - nb * C::BN), nb, num_n, row < p.M, row, first_id,
+                      lists + quarter * 32 + lane, p.Nout);
+      } else if constexpr (EPI == EPI_HEAD_DLOGITS) {
+        head_dlogits_tile(p.head, tbase, min(C::BN, p.Nout - nb * C::BN), p.v0 + nb * C::BN, row < p.M, row,
+                          p.out + static_cast<size_t>(row) * p.Nout + nb * C::BN);
       } else if constexpr (EPI == EPI_ACC_F32) {
         float* arow = p.acc32 + static_cast<size_t>(row) * p.Nout;
         __nv_bfloat16* orow = p.out + static_cast<size_t>(row) * p.Nout;

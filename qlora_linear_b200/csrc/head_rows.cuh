@@ -1,0 +1,230 @@
+// head_rows.cuh — the head's forward (head.cuh) for a few rows: single tokens and decoding
+// batches of up to 128.
+//
+// Bound by HBM: the head W [V, D] is read once, 2·V·D bytes, against 2·M·V·D flops.  One CTA
+// per SM owns a contiguous range of vocabulary entries (multiples of 16, so the ranges differ
+// by at most 16) and walks it in tiles of up to 256 entries; X stays in L2.  Per tile the
+// tensor core computes the 128 × 256 accumulator of all rows (unused rows hold whatever shared
+// memory held; nobody reads them): half of what a CTA pair's 256 rows would cost for the same
+// bytes of W.  The statistics, the candidates and the given tokens' logits stay with the CTA
+// over its whole range, so a row leaves one partial a CTA.
+//
+// W goes through a ring of stages of 64 of the D columns: a full tile in one TMA box of 256
+// entries, a range's last tile in boxes of 16.  The stages' number follows from what the lists
+// and X leave of shared memory (5 for one row, 3 at 128 rows with 32 alternatives).
+// Roles: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warps 2-5 epilogue (thread =
+// row).  Every wait is bounded.
+#pragma once
+
+#include "head.cuh"
+
+namespace lora {
+
+constexpr int HR_ROWS = 128;        // rows at most
+constexpr int HR_BN = 256;          // vocabulary entries a tile
+constexpr int HR_BK = 64;           // of D per stage
+constexpr int HR_UNIT = 16;         // granularity of the CTAs' ranges
+constexpr int HR_MAX_STAGES = 6;
+constexpr int HR_THREADS = 192;
+constexpr int HR_W_BYTES = HR_BN * HR_BK * 2;  // 32 KB
+constexpr int HR_SMEM_MAX = 232448 - 2048;  // dynamic; the barriers are static
+
+// CTAs: one per SM, at least 32 entries each.
+__host__ __device__ constexpr int hr_ctas(long long V) {
+  return static_cast<int>((V + 31) / 32 < 148 ? (V + 31) / 32 : 148);
+}
+// Bytes of X in a stage: the rows rounded up to the 8-row swizzle atom.
+__host__ __device__ constexpr int hr_x_bytes(int M) { return (M + 7) / 8 * 8 * HR_BK * 2; }
+__host__ __device__ constexpr int hr_tail_bytes(int k) { return 256 + k * kHeadListThreads * 8; }
+// Stages that fit; the MMA reads 128 rows of X from any stage, so 16 KB must follow the last
+// stage's X (the tail counts towards them).
+__host__ __device__ constexpr int hr_stages(int M, int k) {
+  const int stage = HR_W_BYTES + hr_x_bytes(M);
+  const int behind = 128 * HR_BK * 2 - hr_x_bytes(M);
+  const int tail = hr_tail_bytes(k) > behind ? hr_tail_bytes(k) : behind;
+  const int n = (HR_SMEM_MAX - 1024 - tail) / stage;
+  return n < HR_MAX_STAGES ? n : HR_MAX_STAGES;
+}
+
+struct HeadRowsParams {
+  HeadArgs h;              // sorted is not used; part/cand are [M][CTAs]
+  const int32_t* ids;      // [M][n]
+  int M, V, D;
+  int stages;
+  uint32_t* status;
+  uint64_t wait_ns;
+};
+
+__global__ void __launch_bounds__(HR_THREADS, 1)
+    head_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmW16, const HeadRowsParams p) {
+  griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
+  extern __shared__ __align__(1024) uint8_t hr_raw[];
+  __shared__ __align__(8) uint64_t full[HR_MAX_STAGES], empty[HR_MAX_STAGES], tfull[2], tempty[2], drain;
+  __shared__ uint32_t tmem_slot, abort_s, never_s;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(hr_raw) + 1023) & ~uintptr_t(1023));
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.stages;
+  const int xbytes = hr_x_bytes(p.M);
+  const int stage_bytes = HR_W_BYTES + xbytes;
+  const int units = (p.V + HR_UNIT - 1) / HR_UNIT;
+  const int r0 = static_cast<int>(static_cast<long long>(units) * blockIdx.x / gridDim.x) * HR_UNIT;
+  const int r1 = static_cast<int>(static_cast<long long>(units) * (blockIdx.x + 1) / gridDim.x) * HR_UNIT;
+  const int ntiles = (r1 - r0 + HR_BN - 1) / HR_BN;
+  const int nkb = (p.D + HR_BK - 1) / HR_BK;
+  const WaitCtl wc{&abort_s, p.status, p.wait_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), 4);
+    }
+    mbar_init(smem_u32(&drain), 1);
+    abort_s = 0;
+    never_s = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmX);
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmW16);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long fills = 0;
+      bool ok = true;
+      for (int t = 0; ok && t < ntiles; ++t) {
+        const int v0 = r0 + t * HR_BN;
+        const int rows = min(HR_BN, r1 - v0);  // a multiple of 16
+        // checked build: the tile starts inside the head and its boxes inside the stage
+        if (!lora_check(v0 < p.V && rows > 0 && rows % HR_UNIT == 0 && p.M <= HR_ROWS && S <= HR_MAX_STAGES, wc)) {
+          ok = false;
+          break;
+        }
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
+          const uint32_t sW = smem_u32(smem + stage * stage_bytes);
+          const uint32_t bar = smem_u32(&full[stage]);
+          mbar_arrive_expect_tx(bar, rows * HR_BK * 2 + xbytes);
+          if (rows == HR_BN) {
+            tma_load_2d(sW, &tmW, bar, kb * HR_BK, v0);
+          } else {
+            for (int u = 0; u < rows; u += HR_UNIT) tma_load_2d(sW + u * HR_BK * 2, &tmW16, bar, kb * HR_BK, v0 + u);
+          }
+          tma_load_2d(sW + HR_W_BYTES, &tmX, bar, kb * HR_BK, 0);
+          ++fills;
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // after an abort, loads still in flight land before shared memory goes away
+      if (!ok) {
+        const WaitCtl drain_wc{&never_s, nullptr, p.wait_ns};
+        for (long long f = fills > S ? fills - S : 0; f < fills; ++f)
+          mbar_wait(smem_u32(&full[f % S]), static_cast<uint32_t>((f / S) & 1), drain_wc);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      int acc = 0;
+      bool ok = true;
+      for (int t = 0; ok && t < ntiles; ++t) {
+        const uint32_t idesc = idesc_bf16_f32(HR_ROWS, min(HR_BN, r1 - r0 - t * HR_BN), false, false);
+        if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, wc)) break;
+        tc_fence_after();
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(smem_u32(&full[stage]), phase, wc)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sW = smem_u32(smem + stage * stage_bytes);
+#pragma unroll
+          for (int k = 0; k < HR_BK / 16; ++k)
+            tc_mma_bf16(tmem_base + acc * HR_BN, sdesc_sw128(sW + HR_W_BYTES + k * 32, 16, 1024),
+                        sdesc_sw128(sW + k * 32, 16, 1024), idesc, (kb > 0 || k > 0) ? 1u : 0u);
+          tc_commit(smem_u32(&empty[stage]));
+          if (++stage == S) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit(smem_u32(&tfull[acc]));
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+      // every MMA issued so far must finish before TMEM is released
+      tc_commit(smem_u32(&drain));
+      const WaitCtl drain_wc{&never_s, nullptr, p.wait_ns};
+      mbar_wait(smem_u32(&drain), 0, drain_wc);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (thread = row)
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const bool in = row < p.M;
+    const HeadArgs& h = p.h;
+    TopList list;
+    list.init(reinterpret_cast<unsigned long long*>(smem + S * stage_bytes) + row, h.k);
+    RowStats st{-INFINITY, 0.0f, 0.0f};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = 0; t < ntiles; ++t) {
+      if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, wc)) { ok = false; break; }
+      tc_fence_after();
+      if (quarter * 32 < p.M) {  // a warp without rows has nothing to read
+        const int v0 = r0 + t * HR_BN;
+        const int nv = min(HR_BN, min(r1, p.V) - v0);
+        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * HR_BN;
+        for (int i = 0; i < h.n; ++i) {
+          int col = -1;
+          if (in) {
+            const uint32_t off = static_cast<uint32_t>(p.ids[static_cast<size_t>(row) * h.n + i]) - static_cast<uint32_t>(v0);
+            if (off < static_cast<uint32_t>(nv)) col = static_cast<int>(off);
+          }
+          uint32_t want = __ballot_sync(0xffffffffu, col >= 0);
+          while (want) {
+            const int at = __shfl_sync(0xffffffffu, col, __ffs(want) - 1);
+            const float z = __uint_as_float(tmem_ld_32x32b_x1(tbase + at)) * h.scale;
+            if (col == at) h.id_logit[static_cast<size_t>(row) * h.n + i] = z;
+            want &= ~__ballot_sync(0xffffffffu, col == at);
+          }
+        }
+        float lower;
+        const float m = head_tile_max(h, tbase, nv, in, nullptr, lower);
+        st = join_stats(st, head_tile_sums(h, tbase, nv, v0, in, m, lower, list, nullptr));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    if (ok && in) {
+      const size_t at = static_cast<size_t>(row) * gridDim.x + blockIdx.x;
+      h.part[at] = make_float4(st.m, st.s, st.t, __int_as_float(list.cnt));
+      for (int i = 0; i < list.cnt; ++i) h.cand[at * h.k + i] = list.s[i * kHeadListThreads];
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+}  // namespace lora

@@ -19,6 +19,7 @@
 #include "elementwise.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_q.cuh"
+#include "head_rows.cuh"
 #include "skinny.cuh"
 #include "streamk.cuh"
 #include "tcproj.cuh"
@@ -376,6 +377,9 @@ lora_status_t dev_info(DevInfo** out) {
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_CE_LSE>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_CE_DLOGITS>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<true, EPI_ACC_F32>), (PairCfg<true>::SMEM_BYTES));
+    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_FWD>), (PairCfg<false>::smem_bytes<EPI_HEAD_FWD>()));
+    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_DLOGITS>), (PairCfg<false>::SMEM_BYTES));
+    SET_SMEM(head_rows_kernel, HR_SMEM_MAX);
     SET_SMEM((rowproj_kernel<16, false>), (rowproj_smem_bytes<16, false>()));
     SET_SMEM((rowproj_kernel<32, false>), (rowproj_smem_bytes<32, false>()));
     SET_SMEM((rowproj_kernel<64, false>), (rowproj_smem_bytes<64, false>()));
@@ -621,8 +625,8 @@ lora_status_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUte
   const int grid = static_cast<int>(2 * (pairs > 0 ? pairs : 1));
   {
     TimedRegion tr(B_MN ? LORA_KERNEL_BWD_GEMM : LORA_KERNEL_FWD_GEMM, st);
-    launch_k(lora_gemm_pair_kernel<B_MN, EPI>, dim3(grid), dim3(C::template threads<EPI>()), C::SMEM_BYTES, st, a, b,
-             e, f, p);
+    launch_k(lora_gemm_pair_kernel<B_MN, EPI>, dim3(grid), dim3(C::template threads<EPI>()),
+             C::template smem_bytes<EPI>(), st, a, b, e, f, p);
   }
   count_launch();
   return last_launch();
@@ -670,8 +674,9 @@ lora_status_t launch_gemm_w(const lora_weight_t* W, const CUtensorMap& a, const 
                             const PairParams& p, int sms, cudaStream_t st) {
   CUtensorMap b, f;
   TRY(tmap_bf16(&f, fs.base, fs.inner, fs.rows, kBoxX, kBoxY));
-  if constexpr (EPI == EPI_CE_LSE || EPI == EPI_CE_DLOGITS || EPI == EPI_ACC_F32) {
-    // the cross-entropy head is bf16 only (checked by the caller)
+  if constexpr (EPI == EPI_CE_LSE || EPI == EPI_CE_DLOGITS || EPI == EPI_ACC_F32 || EPI == EPI_HEAD_FWD ||
+                EPI == EPI_HEAD_DLOGITS) {
+    // the LM head is bf16 only (checked by the caller)
     TRY(tmap_bf16(&b, W->data, W->K, W->N, kBoxX, kBoxY));
     return launch_gemm<B_MN, EPI>(a, b, e, f, p, sms, st);
   } else {
@@ -1179,6 +1184,258 @@ PairParams ce_params(long long M, long long Nout, long long Kred, void* out, uin
   return p;
 }
 
+// ---------------------------------------------------------------- LM head: token log-probabilities, distillation
+// Rows up to which the forward without a saved buffer runs head_rows_kernel (one read of the
+// head, all rows at once) instead of the pair GEMM.
+constexpr long long kHeadFewRows = HR_ROWS;
+// Scratch the forward's per-tile results may take: the rows are worked off in chunks of a
+// multiple of 256 that keep to it (at least 256 rows).
+constexpr size_t kHeadChunkBytes = size_t(512) << 20;
+
+inline int pow2_at_least(int k) {
+  int p = 1;
+  while (p < k) p <<= 1;
+  return p;
+}
+
+// Forward scratch: the chunk's sorted tokens, their logits, the groups' bounds, the partials
+// of every row and tile (or CTA) and the candidates.  Pure functions of the sizes.
+struct HeadFwdLayout {
+  bool few = false;
+  long long chunk = 0;  // rows
+  int np = 0;           // partials a row
+  size_t sorted_off = 0, logit_off = 0, bound_off = 0, part_off = 0, cand_off = 0, total = 0;
+};
+HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save) {
+  HeadFwdLayout l;
+  const int kp = k > 0 ? pow2_at_least(k) : 0;
+  l.few = M <= kHeadFewRows && !save;
+  l.np = l.few ? hr_ctas(V) : cdiv(V, 256);
+  const size_t per_row = 12 * static_cast<size_t>(n) + 4 * kp + static_cast<size_t>(l.np) * (16 + 8 * static_cast<size_t>(k));
+  long long c = static_cast<long long>(kHeadChunkBytes / per_row) / 256 * 256;
+  if (c < 256) c = 256;
+  l.chunk = M < c ? M : c;
+  const size_t R = static_cast<size_t>(l.chunk);
+  l.sorted_off = kStatusBytes;
+  l.logit_off = l.sorted_off + align256(R * n * 8);
+  l.bound_off = l.logit_off + align256(R * n * 4);
+  l.part_off = l.bound_off + align256(R * kp * 4);
+  l.cand_off = l.part_off + align256(R * l.np * 16);
+  l.total = l.cand_off + align256(R * l.np * k * 8);
+  return l;
+}
+
+// Backward scratch: sorted (id, coefficient) pairs and row coefficients of all rows; then
+// either the stream-K slots of a dX GEMM over the whole vocabulary with, unless the logits
+// were saved, dz [M, V] behind them, or the fp32 sum of dX with a slice of dz.
+struct HeadBwdLayout {
+  size_t sorted_off = 0, rowp_off = 0, slot_off = 0, whole_dz_off = 0, acc_off = 0, slice_dz_off = 0;
+};
+HeadBwdLayout head_bwd_layout(long long M, long long D, long long V, int n) {
+  HeadBwdLayout l;
+  l.sorted_off = kStatusBytes;
+  l.rowp_off = l.sorted_off + align256(static_cast<size_t>(M) * n * 8);
+  l.slot_off = l.rowp_off + align256(static_cast<size_t>(M) * 16);
+  l.whole_dz_off = l.slot_off + align256(gemm_sched_bytes(M, D, V, 0, false));
+  l.acc_off = l.slot_off;
+  l.slice_dz_off = l.acc_off + align256(static_cast<size_t>(M) * D * 4);
+  return l;
+}
+
+inline size_t head_tile_max_off(long long M, long long V) { return align256(static_cast<size_t>(M) * V * 2); }
+
+bool head_sizes_ok(long long M, long long D, long long V, int n, int k) {
+  return M >= 0 && M <= (1LL << 31) - 256 && D > 0 && D <= (1LL << 30) && V > 0 && V <= (1LL << 30) && n >= 0 &&
+         n <= kHeadMaxIds && k >= 0 && k <= kHeadMaxTop;
+}
+
+lora_status_t head_check(const void* X, long long M, const lora_weight_t* W, const int32_t* ids, int n, float scale,
+                         const void* saved) {
+  TRY(check_weight(W));
+  if (W->fmt != LORA_W_BF16) return LORA_ERR_UNSUPPORTED;
+  if (M < 0 || M > (1LL << 31) - 256 || n < 0) return LORA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.0f) return LORA_ERR_INVALID_ARG;
+  if (n > kHeadMaxIds) return LORA_ERR_UNSUPPORTED;
+  if (M == 0) return LORA_OK;
+  TRY(check_ptr(X));
+  if (n > 0) TRY(check_ptr(ids));
+  if (saved && !aligned16(saved)) return LORA_ERR_ALIGNMENT;
+  return LORA_OK;
+}
+
+lora_status_t head_workspace(const void* workspace, size_t ws_bytes, size_t need) {
+  if (!workspace) return LORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LORA_ERR_ALIGNMENT;
+  return ws_bytes < need ? LORA_ERR_WORKSPACE : LORA_OK;
+}
+
+// Forward of both operators: `r` holds the caller's outputs (and, for distillation, the
+// teacher's logits) for all rows.
+lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, HeadRowArgs r, void* saved,
+                            void* workspace, size_t ws_bytes, cudaStream_t st) {
+  const long long V = W->N, D = W->K;
+  const int n = r.n, k = r.k;
+  const HeadFwdLayout l = head_fwd_layout(M, V, n, k, saved != nullptr);
+  TRY(head_workspace(workspace, ws_bytes, l.total));
+  DevInfo* dev = nullptr;
+  TRY(dev_info(&dev));
+  TRY(get_encode());
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* status = reinterpret_cast<uint32_t*>(ws);
+  HeadArgs h{};
+  h.scale = r.scale;
+  h.n = n;
+  h.k = k;
+  h.kp = k > 0 ? pow2_at_least(k) : 0;
+  h.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
+  h.id_logit = reinterpret_cast<float*>(ws + l.logit_off);
+  h.bound = reinterpret_cast<unsigned*>(ws + l.bound_off);
+  h.part = reinterpret_cast<float4*>(ws + l.part_off);
+  h.cand = reinterpret_cast<unsigned long long*>(ws + l.cand_off);
+  r.V = static_cast<int>(V);
+  r.kp = h.kp;
+  r.np = l.np;
+  r.part = h.part;
+  r.id_logit = h.id_logit;
+  r.cand = h.cand;
+  r.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
+  r.bound = k > 0 ? h.bound : nullptr;
+  if (l.few) {
+    HeadRowsParams p{};
+    p.h = h;
+    p.ids = r.ids;
+    p.M = static_cast<int>(M);
+    p.V = static_cast<int>(V);
+    p.D = static_cast<int>(D);
+    p.stages = hr_stages(p.M, k);
+    p.status = status;
+    p.wait_ns = wait_limit_ns();
+    CUtensorMap tx, tw, tw16;
+    TRY(tmap_bf16(&tx, X, D, M, HR_BK, static_cast<uint32_t>((M + 7) / 8 * 8)));
+    TRY(tmap_bf16(&tw, W->data, D, V, HR_BK, HR_BN));
+    TRY(tmap_bf16(&tw16, W->data, D, V, HR_BK, HR_UNIT));
+    launch_k(head_rows_kernel, dim3(l.np), dim3(HR_THREADS), HR_SMEM_MAX, st, tx, tw, tw16, p);
+    count_launch();
+    TRY(last_launch());
+    r.M = p.M;
+    launch_k(head_finalize_kernel, dim3(cdiv(M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
+    count_launch();
+    return last_launch();
+  }
+  for (long long m0 = 0; m0 < M; m0 += l.chunk) {
+    const long long m = M - m0 < l.chunk ? M - m0 : l.chunk;
+    const uint8_t* Xc = static_cast<const uint8_t*>(X) + static_cast<size_t>(m0) * D * 2;
+    HeadRowArgs a = r;
+    a.M = static_cast<int>(m);
+    auto at = [&](auto* p, long long per) { return p ? p + m0 * per : p; };
+    a.ids = at(r.ids, n);
+    a.teacher = at(r.teacher, n);
+    a.logprob = at(r.logprob, n);
+    a.entropy = at(r.entropy, 1);
+    a.lse_out = at(r.lse_out, 1);
+    a.loss = at(r.loss, 1);
+    a.top_ids = at(r.top_ids, k);
+    a.top_logprob = at(r.top_logprob, k);
+    if (n > 0 || k > 0) {
+      launch_k(head_prep_kernel<false>, dim3(cdiv(m, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, a);
+      count_launch();
+      TRY(last_launch());
+    }
+    CUtensorMap tx;
+    TRY(tmap_bf16(&tx, Xc, D, m, kBoxX, kBoxY));
+    PairParams p = ce_params(m, V, D, nullptr, status, W);
+    p.head = h;
+    if (saved) {
+      p.head.expz = static_cast<__half*>(saved) + static_cast<size_t>(m0) * V;
+      p.head.tile_max = reinterpret_cast<float*>(static_cast<uint8_t*>(saved) + head_tile_max_off(M, V)) +
+                        static_cast<size_t>(m0) * l.np;
+    }
+    TRY((launch_gemm_w<false, EPI_HEAD_FWD>(W, tx, tx, FSpec{Xc, static_cast<uint64_t>(D), static_cast<uint64_t>(m)}, p,
+                                            dev->sms, st)));
+    launch_k(head_finalize_kernel, dim3(cdiv(m, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, a);
+    count_launch();
+    TRY(last_launch());
+  }
+  return LORA_OK;
+}
+
+// Backward of both operators, over the whole vocabulary at once from a saved forward (whose
+// buffer becomes dz) or where dz [M, V] fits the workspace, else slice by slice.
+lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, HeadRowArgs r, void* saved, void* dX,
+                            void* workspace, size_t ws_bytes, cudaStream_t st) {
+  const long long V = W->N, D = W->K;
+  const int n = r.n, tiles = cdiv(V, 256);
+  // one warp of the pass over a saved buffer per row and 2048 columns
+  const long long jobs = static_cast<long long>(M) * cdiv(tiles, kHeadSpan);
+  if (saved && jobs > (1LL << 31) - 4) return LORA_ERR_UNSUPPORTED;
+  const HeadBwdLayout l = head_bwd_layout(M, D, V, n);
+  const bool whole = saved || ws_bytes >= l.whole_dz_off + static_cast<size_t>(M) * V * 2;
+  TRY(head_workspace(workspace, ws_bytes, whole ? l.whole_dz_off : l.slice_dz_off));
+  long long vc = V;
+  if (!whole) {
+    vc = static_cast<long long>((ws_bytes - l.slice_dz_off) / (static_cast<size_t>(M) * 2)) / 256 * 256;
+    if (vc < 256) return LORA_ERR_WORKSPACE;
+    if (vc > V) vc = V;
+  }
+  DevInfo* dev = nullptr;
+  TRY(dev_info(&dev));
+  TRY(get_encode());
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* status = reinterpret_cast<uint32_t*>(ws);
+  r.M = static_cast<int>(M);
+  r.V = static_cast<int>(V);
+  r.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
+  r.rowp = reinterpret_cast<float4*>(ws + l.rowp_off);
+  launch_k(head_prep_kernel<true>, dim3(cdiv(M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
+  count_launch();
+  TRY(last_launch());
+  HeadArgs h{};
+  h.scale = r.scale;
+  h.n = n;
+  h.sorted = r.sorted;
+  h.rowp = r.rowp;
+  CUtensorMap tx;
+  TRY(tmap_bf16(&tx, X, D, M, kBoxX, kBoxY));
+  auto* dz = saved ? static_cast<__nv_bfloat16*>(saved)
+                   : reinterpret_cast<__nv_bfloat16*>(ws + (whole ? l.whole_dz_off : l.slice_dz_off));
+  const int nslices = static_cast<int>((V + vc - 1) / vc);
+  for (int i = 0; i < nslices; ++i) {
+    const long long v0 = i * vc, w = (V - v0 < vc) ? V - v0 : vc;
+    lora_weight_t Wc = *W;  // rows [v0, v0 + w) of the head
+    Wc.N = w;
+    Wc.data = static_cast<const uint8_t*>(W->data) + static_cast<size_t>(v0) * D * 2;
+    if (saved) {
+      h.expz = static_cast<__half*>(saved);
+      h.tile_max = reinterpret_cast<float*>(static_cast<uint8_t*>(saved) + head_tile_max_off(M, V));
+      launch_k(head_dlogits_saved_kernel, dim3(cdiv(jobs, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, h,
+               static_cast<int>(M), static_cast<int>(V), tiles);
+      count_launch();
+      TRY(last_launch());
+    } else {
+      PairParams p = ce_params(M, w, D, dz, status, &Wc);
+      p.v0 = static_cast<int>(v0);
+      p.head = h;
+      TRY((launch_gemm_w<false, EPI_HEAD_DLOGITS>(
+          &Wc, tx, tx, FSpec{X, static_cast<uint64_t>(D), static_cast<uint64_t>(M)}, p, dev->sms, st)));
+    }
+    CUtensorMap ta;
+    TRY(tmap_bf16(&ta, dz, w, M, kBoxX, kBoxY));
+    const FSpec fs{dz, static_cast<uint64_t>(w), static_cast<uint64_t>(M)};
+    PairParams q = ce_params(M, D, w, dX, status, &Wc);
+    if (whole) {
+      const GemmSched g = set_sched(q, &Wc, reinterpret_cast<float*>(ws + l.slot_off), l.whole_dz_off - l.slot_off,
+                                    dev->sms);
+      TRY((launch_gemm_w<true, EPI_STORE>(&Wc, ta, ta, fs, q, dev->sms, st)));
+      TRY(streamk_fixup(q, g, st));
+    } else {
+      q.acc32 = reinterpret_cast<float*>(ws + l.acc_off);
+      q.acc_mode = (i > 0 ? 1 : 0) | (i == nslices - 1 ? 2 : 0);
+      TRY((launch_gemm_w<true, EPI_ACC_F32>(&Wc, ta, ta, fs, q, dev->sms, st)));
+    }
+  }
+  return LORA_OK;
+}
+
 size_t workspace_bytes_for(int64_t M, int64_t N, int64_t K, int32_t r, int32_t nseg, int32_t fmt) {
   if (M < 0 || N <= 0 || K <= 0 || r < 8 || r > 128 || r % 8) return 0;
   if (nseg < 1 || nseg > LORA_MAX_SEGMENTS || nseg * r > 128) return 0;
@@ -1461,6 +1718,122 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
                                           q, dev->sms, st)));
   }
   return LORA_OK;
+}
+
+size_t lora_head_fwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n, int32_t k) {
+  if (!head_sizes_ok(M, D, V, n, k)) return 0;
+  // a forward with a saved buffer never takes the few-rows kernel: room for either
+  const size_t a = head_fwd_layout(M, V, n, k, false).total, b = head_fwd_layout(M, V, n, k, true).total;
+  return a > b ? a : b;
+}
+
+size_t lora_head_bwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n, int64_t slice) {
+  if (!head_sizes_ok(M, D, V, n, 0) || slice < 0) return 0;
+  const HeadBwdLayout l = head_bwd_layout(M, D, V, n);
+  if (slice == 0) return l.whole_dz_off;
+  if (slice >= V) return l.whole_dz_off + align256(static_cast<size_t>(M) * V * 2);
+  return l.slice_dz_off + align256(static_cast<size_t>(M) * ((slice + 255) / 256 * 256) * 2);
+}
+
+size_t lora_head_saved_bytes(int64_t M, int64_t V) {
+  if (M < 0 || M > (1LL << 31) - 256 || V <= 0 || V > (1LL << 30)) return 0;
+  return head_tile_max_off(M, V) + align256(static_cast<size_t>(M) * cdiv(V, 256) * 4);
+}
+
+lora_status_t lora_logprob_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,
+                               int32_t ignore_index, float scale, int32_t k, float* logprob, float* entropy, float* lse,
+                               int32_t* top_ids, float* top_logprob, void* saved, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  TRY(head_check(X, M, W, ids, n, scale, saved));
+  if (k < 0) return LORA_ERR_INVALID_ARG;
+  if (k > kHeadMaxTop || k > W->N) return LORA_ERR_UNSUPPORTED;
+  if (M == 0) return LORA_OK;
+  if (n > 0) TRY(check_ptr(logprob));
+  if (entropy && !aligned16(entropy)) return LORA_ERR_ALIGNMENT;
+  TRY(check_ptr(lse));
+  if (k > 0) {
+    TRY(check_ptr(top_ids));
+    TRY(check_ptr(top_logprob));
+  }
+  HeadRowArgs r{};
+  r.n = n;
+  r.ignore = ignore_index;
+  r.scale = scale;
+  r.ids = ids;
+  r.k = k;
+  r.logprob = n > 0 ? logprob : nullptr;
+  r.entropy = entropy;
+  r.lse_out = lse;
+  r.top_ids = top_ids;
+  r.top_logprob = top_logprob;
+  return head_fwd_core(X, M, W, r, saved, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+lora_status_t lora_logprob_bwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,
+                               int32_t ignore_index, float scale, const float* lse, const float* entropy,
+                               const float* dlogprob, const float* dentropy, void* saved, void* dX, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  TRY(head_check(X, M, W, ids, n, scale, saved));
+  if (M == 0) return LORA_OK;
+  TRY(check_ptr(lse));
+  if (dlogprob && !aligned16(dlogprob)) return LORA_ERR_ALIGNMENT;
+  if (dentropy) {
+    TRY(check_ptr(dentropy));
+    TRY(check_ptr(entropy));
+  }
+  TRY(check_ptr(dX));
+  HeadRowArgs r{};
+  r.n = dlogprob ? n : 0;
+  r.ignore = ignore_index;
+  r.scale = scale;
+  r.ids = ids;
+  r.lse = lse;
+  r.ent = entropy;
+  r.dlogprob = r.n > 0 ? dlogprob : nullptr;
+  r.dentropy = dentropy;
+  return head_bwd_core(X, M, W, r, saved, dX, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+lora_status_t lora_distill_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids,
+                               const float* teacher_logits, int32_t n, int32_t ignore_index, float scale, float* loss,
+                               float* lse, void* saved, void* workspace, size_t ws_bytes, void* stream) {
+  TRY(head_check(X, M, W, ids, n, scale, saved));
+  if (n < 1) return LORA_ERR_INVALID_ARG;
+  if (M == 0) return LORA_OK;
+  TRY(check_ptr(teacher_logits));
+  TRY(check_ptr(loss));
+  TRY(check_ptr(lse));
+  HeadRowArgs r{};
+  r.n = n;
+  r.ignore = ignore_index;
+  r.scale = scale;
+  r.ids = ids;
+  r.teacher = teacher_logits;
+  r.lse_out = lse;
+  r.loss = loss;
+  return head_fwd_core(X, M, W, r, saved, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+lora_status_t lora_distill_bwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids,
+                               const float* teacher_logits, int32_t n, int32_t ignore_index, float scale,
+                               const float* lse, const float* dloss, void* saved, void* dX, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  TRY(head_check(X, M, W, ids, n, scale, saved));
+  if (n < 1) return LORA_ERR_INVALID_ARG;
+  if (M == 0) return LORA_OK;
+  TRY(check_ptr(teacher_logits));
+  TRY(check_ptr(lse));
+  TRY(check_ptr(dloss));
+  TRY(check_ptr(dX));
+  HeadRowArgs r{};
+  r.n = n;
+  r.ignore = ignore_index;
+  r.scale = scale;
+  r.ids = ids;
+  r.teacher = teacher_logits;
+  r.lse = lse;
+  r.dloss = dloss;
+  return head_bwd_core(X, M, W, r, saved, dX, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
 }
 
 lora_status_t dequant_blockwise4(const lora_weight_t* Wq, void* W_out, void* stream) {

@@ -1,0 +1,243 @@
+"""Layers over a frozen bf16 LM head that never hold the [M, V] logits: log-probabilities of
+given tokens with entropy and top alternatives, and distillation from a teacher's top logits,
+each with its gradient in the hidden states."""
+from __future__ import annotations
+
+import contextlib
+import dataclasses
+
+import torch
+
+from . import binding as _b
+
+
+@dataclasses.dataclass
+class TokenLogProbs:
+    """What :meth:`LoraTokenLogProbs.forward` returns.  ``logprob`` has the shape of the ids
+    given (None without ids); ``entropy`` [M]; ``lse`` [M]; ``top_ids`` int32 and
+    ``top_logprob`` [M, k] (None for k = 0).  ``saved`` belongs to the backward."""
+
+    logprob: torch.Tensor | None
+    lse: torch.Tensor
+    entropy: torch.Tensor | None
+    top_ids: torch.Tensor | None = None
+    top_logprob: torch.Tensor | None = None
+    saved: torch.Tensor | None = None
+
+
+@dataclasses.dataclass
+class DistillLoss:
+    """What :meth:`LoraDistill.forward` returns: ``loss`` [M], ``lse`` [M]; ``saved`` belongs
+    to the backward."""
+
+    loss: torch.Tensor
+    lse: torch.Tensor
+    saved: torch.Tensor | None = None
+
+
+class _HeadLayer:
+    """Checks, streams and workspaces shared by the head's layers.
+
+    A call runs on ``stream`` (default: the current stream of X's device) and takes its outputs
+    and its workspace from that stream's memory, one workspace a stream, so calls on two streams
+    do not meet in it.  A call under CUDA graph capture takes a workspace of its own from the
+    graph's memory.
+    """
+
+    def __init__(self, W: "_b.LoraWeight", ignore_index: int = -100, temperature: float = 1.0, slice_: int = 0):
+        if not float(temperature) > 0.0:
+            raise ValueError("temperature must be positive")
+        if W.fmt != _b.LORA_W_BF16:
+            raise _b.LoraError(_b.LORA_ERR_UNSUPPORTED, "the LM head must be bf16")
+        self.W, self.ignore_index, self.slice = W, int(ignore_index), int(slice_)
+        self.scale = 1.0 / float(temperature)
+        self._ws = {}
+
+    @contextlib.contextmanager
+    def _on(self, X, stream, *inputs):
+        """Runs the body with X's device and ``stream`` current; yields the stream's handle."""
+        if stream is None and X.device.index == torch.cuda.current_device():
+            yield torch.cuda.current_stream().cuda_stream
+            return
+        with torch.cuda.device(X.device):
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=X.device)
+            elif stream is None:
+                stream = torch.cuda.current_stream()
+            if stream != torch.cuda.current_stream():
+                for t in (X, *inputs):
+                    if t is not None:
+                        t.record_stream(stream)
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+    def _workspace(self, nbytes: int, device, stream: int) -> torch.Tensor:
+        if nbytes == 0:
+            raise _b.LoraError(_b.LORA_ERR_UNSUPPORTED, "head workspace")
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            ws[:256].zero_()
+            return ws
+        key = (device.index, stream)
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            ws[:256].zero_()
+            self._ws[key] = ws
+        return ws
+
+    def status(self) -> int:
+        """The first device status that is not LORA_OK of the calls made so far (synchronizes),
+        calls under graph capture aside."""
+        out = _b.LORA_OK
+        for (dev, stream), ws in self._ws.items():
+            with torch.cuda.device(dev):
+                st = _b.lora_device_status(ws, stream)
+            out = st if out == _b.LORA_OK else out
+        return out
+
+    def _hidden(self, X):
+        if not (isinstance(X, torch.Tensor) and X.is_cuda and X.dtype == torch.bfloat16 and X.dim() == 2
+                and X.is_contiguous()):
+            raise ValueError("X must be a contiguous bf16 CUDA tensor [M, D]")
+        if X.shape[1] != self.W.K:
+            raise ValueError(f"X has {X.shape[1]} columns, the head {self.W.K}")
+        if X.device != self.W.data.device:
+            raise ValueError(f"X is on {X.device}, the head on {self.W.data.device}")
+        return X.shape[0]
+
+    @staticmethod
+    def _like(t, name, dtype, shape, device):
+        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape)
+                and t.device == device and t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+        return t
+
+    def _ids(self, ids, M, device, flat):
+        """Checks ids [M, n] (or [M], where ``flat`` allows it); returns n."""
+        if not (isinstance(ids, torch.Tensor) and ids.dim() in ((1, 2) if flat else (2,)) and ids.shape[0] == M):
+            raise ValueError(f"ids must be an int32 tensor [{M}, n]" + (f" or [{M}]" if flat else ""))
+        n = ids.shape[1] if ids.dim() == 2 else 1
+        if not 1 <= n <= _b.LORA_HEAD_MAX_IDS:
+            raise ValueError(f"between 1 and {_b.LORA_HEAD_MAX_IDS} tokens a row")
+        self._like(ids, "ids", torch.int32, ids.shape, device)
+        return n
+
+    def _slice(self, M):
+        """Vocabulary rows a slice of a backward that recomputes: about 1 GiB of dz unless set."""
+        if self.slice > 0:
+            return self.slice
+        return max(256, min(self.W.N, (1 << 30) // (2 * max(M, 1)) // 256 * 256))
+
+    def _saved(self, M, device):
+        return torch.empty(_b.head_saved_bytes(M, self.W.N), dtype=torch.uint8, device=device)
+
+    def _bwd_workspace(self, M, n, saved, device, handle):
+        nb = _b.head_bwd_workspace_bytes(M, self.W.K, self.W.N, n, 0 if saved is not None else self._slice(M))
+        return self._workspace(nb, device, handle)
+
+    def _dX(self, dX, X):
+        if dX is None:
+            return torch.empty_like(X)
+        return self._like(dX, "dX", torch.bfloat16, X.shape, X.device)
+
+
+class LoraTokenLogProbs(_HeadLayer):
+    """Log-probabilities of given tokens under softmax(X·Wᵀ/temperature), with the entropy of
+    each row and its ``top_k`` alternatives, over a frozen bf16 LM head ``W [V, D]`` (a
+    :class:`LoraWeight`), without the ``[M, V]`` logits.
+
+    ``forward(X, ids)``: X bf16 [M, D], ids int32 [M] or [M, n] (n <= 128, entries equal to
+    ``ignore_index`` have logprob 0 and no gradient) or None; top_k <= 32.  With ``save=True`` the
+    forward keeps 2·M·V bytes for one backward, which then skips recomputing the logits (a later
+    backward of the same forward recomputes them, in vocabulary slices of ``slice_`` rows, by
+    default as many as take 1 GiB).  ``backward`` returns dX for upstream gradients of the
+    log-probabilities (shape of ids) and of the entropies ([M]).
+    """
+
+    def forward(self, X: torch.Tensor, ids: torch.Tensor | None = None, top_k: int = 0, entropy: bool = True,
+                save: bool = False, stream=None) -> TokenLogProbs:
+        M, dev = self._hidden(X), X.device
+        n = 0 if ids is None else self._ids(ids, M, dev, True)
+        k = int(top_k)
+        if not 0 <= k <= min(_b.LORA_HEAD_MAX_TOP, self.W.N):
+            raise ValueError(f"top_k must be between 0 and {min(_b.LORA_HEAD_MAX_TOP, self.W.N)}")
+        with self._on(X, stream, ids) as handle:
+            f32 = torch.float32
+            out = TokenLogProbs(
+                None if ids is None else torch.empty(ids.shape, dtype=f32, device=dev),
+                torch.empty(M, dtype=f32, device=dev),
+                torch.empty(M, dtype=f32, device=dev) if entropy else None,
+                torch.empty((M, k), dtype=torch.int32, device=dev) if k else None,
+                torch.empty((M, k), dtype=f32, device=dev) if k else None,
+                self._saved(M, dev) if save else None)
+            ws = self._workspace(_b.head_fwd_workspace_bytes(M, self.W.K, self.W.N, n, k), dev, handle)
+            _b.lora_logprob_fwd(X, M, self.W, ids, n, self.ignore_index, self.scale, k, out.logprob, out.entropy,
+                                out.lse, out.top_ids, out.top_logprob, out.saved, ws, stream=handle)
+        return out
+
+    def backward(self, X: torch.Tensor, ids: torch.Tensor | None, fwd: TokenLogProbs,
+                 dlogprob: torch.Tensor | None = None, dentropy: torch.Tensor | None = None, dX=None,
+                 stream=None) -> torch.Tensor:
+        M, dev = self._hidden(X), X.device
+        n = 0 if ids is None else self._ids(ids, M, dev, True)
+        if dlogprob is not None:
+            if ids is None:
+                raise ValueError("dlogprob without ids")
+            self._like(dlogprob, "dlogprob", torch.float32, ids.shape, dev)
+        if dentropy is not None:
+            if fwd.entropy is None:
+                raise ValueError("dentropy needs a forward with entropy=True")
+            self._like(dentropy, "dentropy", torch.float32, (M,), dev)
+        self._like(fwd.lse, "the forward's lse", torch.float32, (M,), dev)
+        with self._on(X, stream, ids, dlogprob, dentropy, fwd.lse, fwd.entropy, fwd.saved) as handle:
+            dX = self._dX(dX, X)
+            saved, fwd.saved = fwd.saved, None  # the backward overwrites it
+            ws = self._bwd_workspace(M, n, saved, dev, handle)
+            _b.lora_logprob_bwd(X, M, self.W, ids, n, self.ignore_index, self.scale, fwd.lse, fwd.entropy, dlogprob,
+                                dentropy, saved, dX, ws, stream=handle)
+        return dX
+
+
+class LoraDistill(_HeadLayer):
+    """Distillation from a teacher's top logits: per row, KL(q || softmax(X·Wᵀ/temperature))
+    with q the softmax of the listed teacher logits over the same temperature, over a frozen bf16
+    LM head ``W [V, D]``, without the ``[M, V]`` logits.
+
+    ``forward(X, ids, teacher_logits)``: X bf16 [M, D]; ids int32 [M, n] and teacher_logits fp32
+    [M, n] (n <= 128; log-probabilities serve as well, e.g. the ``top_ids`` and ``top_logprob`` of
+    :class:`LoraTokenLogProbs` on the teacher's head).  Entries whose id is ``ignore_index`` are left
+    out; a row without any has loss 0 and no gradient.  ``save`` and ``slice_`` as for
+    :class:`LoraTokenLogProbs`.  ``backward`` returns the gradient of Σ dloss·loss in X.
+    """
+
+    def _teacher(self, ids, teacher_logits, M, dev):
+        n = self._ids(ids, M, dev, False)
+        self._like(teacher_logits, "teacher_logits", torch.float32, (M, n), dev)
+        return n
+
+    def forward(self, X: torch.Tensor, ids: torch.Tensor, teacher_logits: torch.Tensor, save: bool = False,
+                stream=None) -> DistillLoss:
+        M, dev = self._hidden(X), X.device
+        n = self._teacher(ids, teacher_logits, M, dev)
+        with self._on(X, stream, ids, teacher_logits) as handle:
+            out = DistillLoss(torch.empty(M, dtype=torch.float32, device=dev),
+                              torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, dev) if save else None)
+            ws = self._workspace(_b.head_fwd_workspace_bytes(M, self.W.K, self.W.N, n), dev, handle)
+            _b.lora_distill_fwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, out.loss, out.lse,
+                                out.saved, ws, stream=handle)
+        return out
+
+    def backward(self, X: torch.Tensor, ids: torch.Tensor, teacher_logits: torch.Tensor, fwd: DistillLoss,
+                 dloss: torch.Tensor, dX=None, stream=None) -> torch.Tensor:
+        M, dev = self._hidden(X), X.device
+        n = self._teacher(ids, teacher_logits, M, dev)
+        self._like(dloss, "dloss", torch.float32, (M,), dev)
+        self._like(fwd.lse, "the forward's lse", torch.float32, (M,), dev)
+        with self._on(X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved) as handle:
+            dX = self._dX(dX, X)
+            saved, fwd.saved = fwd.saved, None  # the backward overwrites it
+            ws = self._bwd_workspace(M, n, saved, dev, handle)
+            _b.lora_distill_bwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, fwd.lse, dloss,
+                                saved, dX, ws, stream=handle)
+        return dX

@@ -15,5 +15,7 @@ from .inputs import (  # noqa: F401
     make_mlp_case,
     CeCase,
     make_ce_case,
+    HeadCase,
+    make_head_case,
     config_cases,
 )

@@ -291,3 +291,43 @@ def make_ce_case(case: CeCase) -> dict:
     labels[g.random(M) < case.ignore_frac] = case.ignore_index
     dloss = (0.5 + g.random(M)).astype(np.float32)
     return {"case": case, "X": X, "W": W, "labels": labels, "dloss": dloss}
+
+
+@dataclasses.dataclass(frozen=True)
+class HeadCase:
+    """Given tokens (or a teacher's list) over an LM head: M rows of hidden states of width D,
+    vocabulary V, n tokens a row."""
+
+    name: str
+    M: int
+    D: int
+    V: int
+    n: int
+    seed: int
+    ignore_index: int = -100
+    ignore_frac: float = 0.1
+
+
+def make_head_case(case: HeadCase) -> dict:
+    """Hidden states of unit variance and a head giving logits of standard deviation about 2,
+    both on power-of-two grids (X on 1/16, W on 2^(floor(log2 2/√D) - 4)), so that a sum of their
+    products is exact in fp32 in any order and the order of the logits is that of the exact ones.
+    Every third row leans towards its first token.  ids uniform on [0, V), a fraction of rows and
+    of entries set to ignore_index; teacher logits N(0, 4); upstream gradients N(0, 1)."""
+    M, D, V, n = case.M, case.D, case.V, case.n
+    g = np.random.Generator(np.random.PCG64(np.random.SeedSequence([case.seed, 9])))
+    std = 2.0 / np.sqrt(D)
+    step = 2.0 ** (np.floor(np.log2(std)) - 4)
+    Wi = np.clip(np.rint(g.standard_normal((V, D)) * (std / step)), -250, 250)
+    ids = g.integers(0, V, (M, n)).astype(np.int32)
+    X = g.standard_normal((M, D))
+    if n:
+        X[::3] += (4.0 / np.sqrt(D)) * (step / std) * Wi[ids[::3, 0]]
+    Xi = np.clip(np.rint(X * 16), -250, 250)
+    ids[g.random((M, n)) < case.ignore_frac / 2] = case.ignore_index
+    ids[g.random(M) < case.ignore_frac / 2] = case.ignore_index
+    return {"case": case, "X": bf16_bits_from_f32((Xi / 16).astype(np.float32)),
+            "W": bf16_bits_from_f32((Wi * step).astype(np.float32)), "ids": ids,
+            "teacher": (2.0 * g.standard_normal((M, n))).astype(np.float32),
+            "dlogprob": g.standard_normal((M, n)).astype(np.float32),
+            "dentropy": g.standard_normal(M).astype(np.float32), "dloss": (0.5 + g.random(M)).astype(np.float32)}
