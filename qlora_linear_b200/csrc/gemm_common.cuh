@@ -14,8 +14,9 @@ struct HeadArgs {
   float* id_logit;           // forward: [M][n]
   int k, kp;                 // alternatives a row, and the power of two >= k of their groups
   unsigned* bound;           // forward: [M][kp] group maxima over the tiles seen so far
-  unsigned long long* cand;  // forward: [M][tiles][k] candidate keys
-  float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, candidates)
+  float* cmax;               // forward: [M][tiles · chunks] maxima of every 32 columns
+  float* zlog;               // forward: [M][V] logits of the chunks that may matter
+  float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, own bound)
   __half* expz;              // [M][V] e^{z - tile max}, or null
   float* tile_max;           // [M][tiles], with expz
   const float4* rowp;        // backward: [M] (lse, Σc + g_H·H, g_H, -)

@@ -50,9 +50,12 @@ struct PairCfg {
   static constexpr int NUM_THREADS = 32 * (2 + NUM_EPI_WARPS);
   // The SwiGLU-backward epilogue reads the saved gate and up values and rewrites them (four
   // times the bytes of a plain store): two warps per TMEM lane quarter, each draining half
-  // of the columns, keep twice the loads in flight.
+  // of the columns, keep twice the loads in flight.  The head's epilogues are bound by the latency
+  // of exp in one warp a scheduler, and take two as well.
   template <int EPI>
-  static constexpr int epi_warps() { return EPI == EPI_SWIGLU_BWD ? 8 : NUM_EPI_WARPS; }
+  static constexpr int epi_warps() {
+    return EPI == EPI_SWIGLU_BWD || EPI == EPI_HEAD_FWD || EPI == EPI_HEAD_DLOGITS ? 8 : NUM_EPI_WARPS;
+  }
   template <int EPI>
   static constexpr int threads() { return 32 * (2 + epi_warps<EPI>()); }
   static constexpr int TMEM_COLS = 512;
@@ -60,13 +63,6 @@ struct PairCfg {
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 8 * NUM_BARS + 16;
   static_assert(STAGE_BYTES % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
-  // The head's forward keeps each thread's best keys behind the barriers (8-byte slots).
-  static constexpr int LIST_OFF = STAGES * STAGE_BYTES + 8 * NUM_BARS + 16;
-  template <int EPI>
-  static constexpr int smem_bytes() {
-    return EPI == EPI_HEAD_FWD ? SMEM_BYTES + kHeadMaxTop * kHeadListThreads * 8 : SMEM_BYTES;
-  }
-  static_assert(LIST_OFF % 8 == 0 && SMEM_BYTES + kHeadMaxTop * kHeadListThreads * 8 <= 232448, "shared memory");
 };
 
 template <bool B_MN, int EPI>
@@ -264,10 +260,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       int mb, nb;
       pair_tile_coords(un.t, num_m, num_n, p.group_m, mb, nb);
       const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
-      int first_id = 0;
-      if constexpr (EPI == EPI_HEAD_FWD) {  // found while the accumulator fills
-        if (row < p.M && p.head.n > 0)
-          first_id = head_first_id(p.head.sorted + static_cast<size_t>(row) * p.head.n, p.head.n, nb * C::BN);
+      // the head's epilogues: this warp's 128 columns, and the row's first given token at or
+      // above them, found while the accumulator fills
+      const int half = NEPI == 8 ? (warp - 2) >> 2 : 0;
+      const int hcol = nb * C::BN + half * kHeadTile;
+      const int2* sorted = nullptr;
+      int pos = 0;
+      int2 first = make_int2(0x7fffffff, 0);
+      float4 rowp = make_float4(0.f, 0.f, 0.f, 0.f);
+      if constexpr (EPI == EPI_HEAD_FWD || EPI == EPI_HEAD_DLOGITS) {
+        if (row < p.M) {
+          sorted = p.head.sorted + static_cast<size_t>(row) * p.head.n;
+          pos = head_first_id(sorted, p.head.n, p.v0 + hcol);
+          if (pos < p.head.n) first = sorted[pos];
+          if (EPI == EPI_HEAD_DLOGITS) rowp = p.head.rowp[row];
+        }
       }
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, wc)) break;
       tc_fence_after();
@@ -286,7 +293,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
         }
       } else if constexpr (EPI == EPI_SWIGLU_BWD) {
         // with 8 epilogue warps, warps 2-5 and 6-9 split the 8 column chunks
-        const int half = (warp - 2) >> 2;
         epi_swiglu_bwd_row(p, tbase, row, nb * C::BN, NEPI == 8 ? 4 * half : 0, NEPI == 8 ? 4 * half + 4 : 8);
       } else if constexpr (EPI == EPI_STORE) {
 #pragma unroll 1
@@ -374,12 +380,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
           }
         }
       } else if constexpr (EPI == EPI_HEAD_FWD) {
-        auto* lists = reinterpret_cast<unsigned long long*>(smem + C::LIST_OFF);
-        head_fwd_tile(p.head, tbase, min(C::BN, p.Nout - nb * C::BN), nb, num_n, row < p.M, row, first_id,
-                      lists + quarter * 32 + lane, p.Nout);
+        if (hcol < p.Nout)  // warp-uniform
+          head_fwd_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), hcol / kHeadTile,
+                        (p.Nout + kHeadTile - 1) / kHeadTile, row < p.M, row, pos, first, p.Nout);
       } else if constexpr (EPI == EPI_HEAD_DLOGITS) {
-        head_dlogits_tile(p.head, tbase, min(C::BN, p.Nout - nb * C::BN), p.v0 + nb * C::BN, row < p.M, row,
-                          p.out + static_cast<size_t>(row) * p.Nout + nb * C::BN);
+        if (hcol < p.Nout)  // warp-uniform
+          head_dlogits_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), p.v0 + hcol, row < p.M,
+                            rowp, sorted, pos, first, p.out + static_cast<size_t>(row) * p.Nout + hcol);
       } else if constexpr (EPI == EPI_ACC_F32) {
         float* arow = p.acc32 + static_cast<size_t>(row) * p.Nout;
         __nv_bfloat16* orow = p.out + static_cast<size_t>(row) * p.Nout;

@@ -10,10 +10,17 @@
 // for upstream gradients c_i of lp_i and g_H of H.  Distillation over a teacher's list is the
 // case c_i = -g·q_i, g_H = 0 (q the softmax of the listed teacher logits).
 //
-// A tile (256 vocabulary entries of one row, in one thread) leaves (m, Σe, Σd·e) with
+// A tile (128 vocabulary entries of one row, in one thread) leaves (m, Σe, Σd·e) with
 // m = max z, d = z - m, e = e^d.  Both sums stay well conditioned: the entropy of the tile is
 // log Σe - Σd·e/Σe, a sum of non-negative terms, and tiles are joined by
 // Σe ← e^{m-M}·Σe, Σd·e ← e^{m-M}·(Σd·e + (m - M)·Σe).
+//
+// The alternatives.  Every 32 columns (a chunk) leave their maximum, and their 32 logits only
+// if that reaches a lower bound of the row's k-th largest logit; head_finalize_top_kernel then
+// looks at the few chunks that reach the final bound.  The bound: cut what was seen so far into
+// kp >= k disjoint groups; the least of the groups' maxima is at most the k-th largest.  It
+// never falls, so a chunk that reaches a later bound has been written.  In random order about
+// k·log k chunks of the whole vocabulary reach it.
 #pragma once
 
 #include "gemm_common.cuh"
@@ -21,8 +28,8 @@
 namespace lora {
 
 constexpr int kHeadMaxIds = 128;   // given tokens (or teacher entries) a row
-constexpr int kHeadMaxTop = 32;    // alternatives a row: one warp lane each
-constexpr int kHeadListThreads = 128;
+constexpr int kHeadMaxTop = 32;    // alternatives a row
+constexpr int kHeadTile = 128;     // columns of a partial of the pair kernel
 
 // ---------------------------------------------------------------- keys of the alternatives
 // Larger key = larger logit, and among equal logits the smaller id.  -0 counts as +0; the
@@ -37,47 +44,6 @@ __device__ __forceinline__ float unord_f32(uint32_t o) {
 __device__ __forceinline__ unsigned long long top_key(float z, int id) {
   return (static_cast<unsigned long long>(ord_f32(z)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
 }
-
-// The k best keys one thread has seen, unsorted, in shared memory ([slot][thread]: no bank
-// conflicts), with the smallest of them once the list is full.
-struct TopList {
-  unsigned long long* s;  // this thread's column
-  int k, cnt, minpos;
-  unsigned long long minkey;
-  __device__ __forceinline__ void init(unsigned long long* col, int k_) {
-    s = col;
-    k = k_;
-    cnt = 0;
-    minpos = 0;
-    minkey = 0;
-  }
-  // Logits below this cannot enter: an equal one has a larger id than the list's.
-  __device__ __forceinline__ float enters_from() const {
-    if (cnt < k) return -INFINITY;
-    return unord_f32(static_cast<uint32_t>(minkey >> 32) + 1u);
-  }
-  __device__ __forceinline__ void rescan() {
-    minkey = s[0];
-    minpos = 0;
-    for (int i = 1; i < k; ++i) {
-      const unsigned long long x = s[i * kHeadListThreads];
-      if (x < minkey) {
-        minkey = x;
-        minpos = i;
-      }
-    }
-  }
-  __device__ __forceinline__ void offer(float z, int id) {
-    const unsigned long long key = top_key(z, id);
-    if (cnt < k) {
-      s[cnt * kHeadListThreads] = key;
-      if (++cnt == k) rescan();
-    } else if (key > minkey) {
-      s[minpos * kHeadListThreads] = key;
-      rescan();
-    }
-  }
-};
 
 struct RowStats {
   float m, s, t;  // max z, Σ e^{z-m}, Σ (z-m)·e^{z-m}
@@ -94,135 +60,104 @@ __device__ __forceinline__ RowStats join_stats(const RowStats& a, const RowStats
 }
 
 // ---------------------------------------------------------------- one accumulator tile
-// First pass over a row's nv <= 256 accumulator columns at tbase: the largest logit and, for
-// the alternatives, a bound.  The columns fall into kp >= k disjoint groups (column mod kp);
-// the least of the groups' maxima is at most the kp-th largest logit, so nothing below it is
-// among the k best.  `bound` (pair kernel) holds the groups' maxima over every tile of the
-// row seen so far, raised by atomic max: which tiles got there first changes how many
-// candidates are kept, never which k remain in the end.
-__device__ __forceinline__ float head_tile_max(const HeadArgs& h, uint32_t tbase, int nv, bool in, unsigned* bound,
-                                               float& lower) {
+// First pass over a row's nv <= 32·NC accumulator columns at tbase: the chunks' maxima
+// (-inf past nv), scaled.  Returns the tile's.
+template <int NC>
+__device__ __forceinline__ float head_tile_max(uint32_t tbase, int nv, float scale, float (&cm)[NC]) {
   float m = -INFINITY;
-  lower = -INFINITY;
-  if (h.k == 0) {
-#pragma unroll 1
-    for (int c = 0; c * 32 < nv; ++c) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    cm[c] = -INFINITY;
+    if (c * 32 < nv) {  // warp-uniform
       uint32_t v[32];
       tmem_ld_32x32b_x32(tbase + c * 32, v);
       tmem_ld_wait();
       const int n = nv - c * 32;
-      if (n >= 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) m = fmaxf(m, __uint_as_float(v[j]));
-      } else {
+      if (n < 32) {  // the vocabulary's last chunk
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (j < n) m = fmaxf(m, __uint_as_float(v[j]));
+          if (j >= n) v[j] = 0xff800000u;
       }
-    }
-    return m * h.scale;
-  }
-  float g[32];
+      float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) g[j] = -INFINITY;
-#pragma unroll 1
-  for (int c = 0; c * 32 < nv; ++c) {
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(tbase + c * 32, v);
-    tmem_ld_wait();
-    const int n = nv - c * 32;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) g[j] = fmaxf(g[j], __uint_as_float(v[j]));
-  }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1)
-    if (h.kp <= s) {
-#pragma unroll
-      for (int j = 0; j < s; ++j) g[j] = fmaxf(g[j], g[j + s]);
-    }
-  uint32_t low = 0xffffffffu;
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < h.kp) {
-      m = fmaxf(m, g[j]);
-      uint32_t o = ord_f32(g[j] * h.scale);
-      if (bound != nullptr && in) {
-        const uint32_t b = __ldcg(bound + j);
-        if (o > b) atomicMax(bound + j, o);
-        o = max(o, b);
+      for (int j = 2; j < 32; j += 2) {
+        a = fmaxf(a, __uint_as_float(v[j]));
+        b = fmaxf(b, __uint_as_float(v[j + 1]));
       }
-      low = min(low, o);
+      cm[c] = fmaxf(a, b) * scale;
+      m = fmaxf(m, cm[c]);
     }
-  lower = unord_f32(low);
-  return m * h.scale;
+  }
+  return m;
 }
 
-// Second pass: the sums, the candidates for the alternatives and (expz != null) e^{z-m} for
-// the backward, in fp16: at most 1, so its 11 bits beat bf16's 8 down to 2^-15, and what lies
-// below weighs less in dX than the rounding of the tile's largest entry.  Columns that few lanes want (a candidate, below: a given token) are
-// read again from TMEM one at a time by the whole warp, since a register cannot be indexed.
-__device__ __forceinline__ RowStats head_tile_sums(const HeadArgs& h, uint32_t tbase, int nv, int v0, bool in, float m,
-                                                   float lower, TopList& list, __half* expz) {
-  float s0 = 0.0f, s1 = 0.0f, t0 = 0.0f, t1 = 0.0f;
+// Second pass: the sums and, of the chunks in `hits`, the logits (zrow != null); expz != null
+// keeps e^{z-m} for the backward, in fp16: at most 1, so its 11 bits beat bf16's 8 down to
+// 2^-15, and what lies below weighs less in dX than the rounding of the tile's largest entry.
+// Full chunks run without a branch: one warp a scheduler hides the latency of exp by the
+// instructions of its other columns alone (with a test per pair of columns the pass took three
+// times as long).
+__device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float scale, bool in, float m, uint32_t hits,
+                                                   float* zrow, __half* expz) {
+  float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
 #pragma unroll 1
   for (int c = 0; c * 32 < nv; ++c) {
     uint32_t v[32];
     tmem_ld_32x32b_x32(tbase + c * 32, v);
     tmem_ld_wait();
     const int n = nv - c * 32;
-    uint32_t mask = 0;
-    if (h.k > 0) {
-      const float from = in ? fmaxf(lower, list.enters_from()) : INFINITY;
-      float cm = -INFINITY;
+    if ((hits >> c) & 1u) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) cm = fmaxf(cm, __uint_as_float(v[j]));
-      if (in && cm * h.scale >= from) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j < n && __uint_as_float(v[j]) * h.scale >= from) mask |= 1u << j;
-      }
-      __syncwarp();
+      for (int q = 0; q < 8; ++q)
+        if (q * 4 < n)
+          *reinterpret_cast<float4*>(zrow + c * 32 + q * 4) =
+              make_float4(__uint_as_float(v[4 * q]) * scale, __uint_as_float(v[4 * q + 1]) * scale,
+                          __uint_as_float(v[4 * q + 2]) * scale, __uint_as_float(v[4 * q + 3]) * scale);
     }
+    if (n >= 32) {
+      float e[32];
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      if (j < n) {  // nv is even (a multiple of 8)
-        const float d0 = __uint_as_float(v[j]) * h.scale - m, d1 = __uint_as_float(v[j + 1]) * h.scale - m;
-        const float e0 = __expf(d0), e1 = __expf(d1);
-        s0 += e0;
-        s1 += e1;
-        t0 = fmaf(d0, e0, t0);
-        t1 = fmaf(d1, e1, t1);
-        v[j >> 1] = pack_f16x2(e0, e1);
+      for (int j = 0; j < 32; ++j) {
+        const float d = fmaf(__uint_as_float(v[j]), scale, -m);
+        e[j] = __expf(d);
+        s[j & 1] += e[j];
+        t[j & 1] = fmaf(d, e[j], t[j & 1]);
       }
-    }
-    if (expz != nullptr && in) {
+      if (expz != nullptr && in) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(expz + c * 32 + q * 8) =
+              make_uint4(pack_f16x2(e[8 * q], e[8 * q + 1]), pack_f16x2(e[8 * q + 2], e[8 * q + 3]),
+                         pack_f16x2(e[8 * q + 4], e[8 * q + 5]), pack_f16x2(e[8 * q + 6], e[8 * q + 7]));
+      }
+    } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (q * 8 < n)
-          *reinterpret_cast<uint4*>(expz + c * 32 + q * 8) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        if (q * 8 < n) {  // n is a multiple of 8
+          float e[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = fmaf(__uint_as_float(v[8 * q + j]), scale, -m);
+            e[j] = __expf(d);
+            s[j & 1] += e[j];
+            t[j & 1] = fmaf(d, e[j], t[j & 1]);
+          }
+          if (expz != nullptr && in)
+            *reinterpret_cast<uint4*>(expz + c * 32 + q * 8) = make_uint4(
+                pack_f16x2(e[0], e[1]), pack_f16x2(e[2], e[3]), pack_f16x2(e[4], e[5]), pack_f16x2(e[6], e[7]));
+        }
     }
-    if (h.k > 0) {
-      uint32_t want = __reduce_or_sync(0xffffffffu, mask);
-      while (want) {
-        const int j = __ffs(want) - 1;
-        want &= want - 1;
-        const float z = __uint_as_float(tmem_ld_32x32b_x1(tbase + c * 32 + j)) * h.scale;
-        if ((mask >> j) & 1u) list.offer(z, v0 + c * 32 + j);
-        __syncwarp();
-      }
-    }
+    __syncwarp();
   }
-  return RowStats{m, s0 + s1, t0 + t1};
+  return RowStats{m, s[0] + s[1], t[0] + t[1]};
 }
 
 // The logits of the row's given tokens that fall into columns [v0, v0 + nv).  sorted: the
-// row's (id, position) by id, pos: the first of them at or above v0.
-__device__ __forceinline__ void head_tile_ids(const HeadArgs& h, uint32_t tbase, int nv, int v0, bool in, int row,
-                                              int pos) {
+// row's (id, position) by id, e: the first of them at or above v0 (pos: its index).  A register
+// cannot be indexed, so the warp reads each wanted column again from TMEM.
+__device__ __forceinline__ void head_tile_ids(const HeadArgs& h, uint32_t tbase, int nv, int v0, int row, int pos,
+                                              int2 e) {
   const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
-  int2 e = in && pos < h.n ? sorted[pos] : make_int2(0x7fffffff, 0);
   while (true) {
     const uint32_t want = __ballot_sync(0xffffffffu, e.x < v0 + nv);
     if (!want) return;
@@ -247,50 +182,74 @@ __device__ __forceinline__ int head_first_id(const int2* sorted, int n, int v0) 
   return lo;
 }
 
-// The pair kernel's forward epilogue of one tile (all lanes of the warp take part).
-__device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase, int nv, int nb, int num_n, bool in,
-                                              int row, int first_id, unsigned long long* list_col, int ldz) {
-  unsigned* bound = h.k > 0 && in ? h.bound + static_cast<size_t>(row) * h.kp : nullptr;
-  float lower;
-  const float m = head_tile_max(h, tbase, nv, in, bound, lower);
-  TopList list;
-  list.init(list_col, h.k);
-  __half* expz = h.expz != nullptr ? h.expz + static_cast<size_t>(row) * ldz + nb * 256 : nullptr;
-  const RowStats st = head_tile_sums(h, tbase, nv, nb * 256, in, m, lower, list, expz);
-  if (h.n > 0) head_tile_ids(h, tbase, nv, nb * 256, in, row, first_id);
+// The pair kernel's forward epilogue of one row's columns [nt·128, +128) (all lanes of the warp
+// take part).  The bound's groups are the chunks modulo kp, over every tile of the row so far,
+// in h.bound: which tiles got there first changes how many chunks are written, never the k best
+// of them.
+__device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase, int nv, int nt, int np, bool in,
+                                              int row, int pos, int2 first, int V) {
+  constexpr int NC = kHeadTile / 32;
+  float cm[NC];
+  const float m = head_tile_max<NC>(tbase, nv, h.scale, cm);
+  const size_t at = static_cast<size_t>(row) * np + nt;
+  uint32_t hits = 0;
+  if (h.k > 0 && in) {
+    unsigned* bound = h.bound + static_cast<size_t>(row) * h.kp;
+    uint32_t low = 0xffffffffu;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const uint32_t o = ord_f32(cm[c]);
+      unsigned* b = bound + ((nt * NC + c) & (h.kp - 1));
+      if (o > __ldcg(b)) atomicMax(b, o);
+    }
+    if (h.kp >= 4) {
+      for (int j = 0; j < h.kp; j += 4) {
+        const uint4 b = __ldcg(reinterpret_cast<const uint4*>(bound + j));
+        low = min(min(low, min(b.x, b.y)), min(b.z, b.w));
+      }
+    } else {
+      for (int j = 0; j < h.kp; ++j) low = min(low, __ldcg(bound + j));
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (ord_f32(cm[c]) >= low && c * 32 < nv) hits |= 1u << c;
+    *reinterpret_cast<float4*>(h.cmax + at * NC) = make_float4(cm[0], cm[1], cm[2], cm[3]);
+  }
+  __syncwarp();
+  const size_t col0 = static_cast<size_t>(row) * V + nt * kHeadTile;
+  const RowStats st = head_tile_sums(tbase, nv, h.scale, in, m, hits, h.zlog + col0,
+                                     h.expz != nullptr ? h.expz + col0 : nullptr);
+  if (h.n > 0) head_tile_ids(h, tbase, nv, nt * kHeadTile, row, pos, first);
   if (!in) return;
-  const size_t at = static_cast<size_t>(row) * num_n + nb;
-  h.part[at] = make_float4(st.m, st.s, st.t, __int_as_float(list.cnt));
+  h.part[at] = make_float4(st.m, st.s, st.t, 0.0f);
   if (h.expz != nullptr) h.tile_max[at] = st.m;
-  for (int i = 0; i < list.cnt; ++i) h.cand[at * h.k + i] = list.s[i * kHeadListThreads];
 }
 
-// dz of one accumulator tile in bf16 (recomputed logits).  rowp: (lse, Σc + g_H·H, g_H).
-__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, bool in, int row,
+// dz of one accumulator tile of nv <= 128 columns in bf16 (recomputed logits).
+// rowp: (lse, Σc + g_H·H, g_H).
+__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, bool in,
+                                                  const float4& rp, const int2* sorted, int pos, int2 e,
                                                   __nv_bfloat16* orow) {
-  float4 rp = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
-  int pos = h.n;
-  if (in) {
-    rp = h.rowp[row];
-    pos = head_first_id(sorted, h.n, v0);
-  }
-  int2 e = pos < h.n ? sorted[pos] : make_int2(0x7fffffff, 0);
 #pragma unroll 1
   for (int c = 0; c * 32 < nv; ++c) {
     uint32_t v[32];
     tmem_ld_32x32b_x32(tbase + c * 32, v);
     tmem_ld_wait();
-    const int n = nv - c * 32;
+    const int n = min(32, nv - c * 32);
     if (in) {
       float d[32];
+      if (rp.z == 0.0f) {
+        const float w = -h.scale * rp.y;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float lp = __uint_as_float(v[j]) * h.scale - rp.x;
-        const float w = rp.z != 0.0f ? fmaf(rp.z, lp, rp.y) : rp.y;
-        d[j] = -h.scale * __expf(lp) * w;
+        for (int j = 0; j < 32; ++j) d[j] = w * __expf(fmaf(__uint_as_float(v[j]), h.scale, -rp.x));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float lp = fmaf(__uint_as_float(v[j]), h.scale, -rp.x);
+          d[j] = -h.scale * __expf(lp) * fmaf(rp.z, lp, rp.y);
+        }
       }
-      while (e.x < v0 + c * 32 + n && e.x < v0 + c * 32 + 32) {
+      while (e.x < v0 + c * 32 + n) {
         const int at = e.x - v0 - c * 32;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
@@ -359,7 +318,10 @@ struct HeadRowArgs {
   int np;
   const float* id_logit;   // [M][n]
   int k, kp;
-  const unsigned long long* cand;
+  int cpp;                 // chunks a partial
+  int few;                 // partials are head_rows_kernel's (col0 of hr_first), else 128 columns each
+  const float* cmax;       // [M][np·cpp] chunk maxima (-inf past a partial's last)
+  const float* zlog;       // [M][V] logits of the chunks that were kept
   float* logprob;          // [M][n] or null
   float* entropy;          // [M] or null
   float* lse_out;          // [M]
@@ -434,38 +396,21 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
   if (!BWD && a.bound != nullptr && lane < a.kp) a.bound[static_cast<size_t>(row) * a.kp + lane] = 0u;
 }
 
-// Descending bitonic sort of size (a power of two) keys in shared memory by one warp.
-__device__ __forceinline__ void warp_sort_desc(unsigned long long* s, int size, int lane) {
-  for (int k = 2; k <= size; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = lane; i < size / 2; i += 32) {
-        const int a = ((i & ~(j - 1)) << 1) | (i & (j - 1)), b = a | j;
-        const unsigned long long x = s[a], y = s[b];
-        if ((x < y) == ((a & k) == 0)) {
-          s[a] = y;
-          s[b] = x;
-        }
-      }
-      __syncwarp();
-    }
+// First vocabulary entry of partial i of np of head_rows_kernel: ranges of multiples of 16.
+__host__ __device__ __forceinline__ int hr_first(int V, int i, int np) {
+  return static_cast<int>(static_cast<long long>((V + 15) / 16) * i / np) * 16;
 }
 
 // One warp a row: joins the row's partials (in a fixed order), and from them the
-// log-probabilities, the entropy, the distillation loss and the alternatives.  The k best
-// among the partials' candidates: a bound from the partials' maxima (groups as in
-// head_tile_max) drops most of them; the rest pass through a buffer of 256 keys that is
-// sorted and cut back to k whenever it fills.
-constexpr int kHeadBuf = 256;
+// log-probabilities, the entropy and the distillation loss.
 __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const HeadRowArgs a) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
-  __shared__ unsigned long long buf_s[kHeadRowWarps][kHeadBuf];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kHeadRowWarps + w;
   if (row >= a.M) return;  // whole warps
   const float4* part = a.part + static_cast<size_t>(row) * a.np;
   float m = -INFINITY;
   for (int i = lane; i < a.np; i += 32) m = fmaxf(m, part[i].x);
-  const float lane_max = m;
   m = warp_max(m);
   float s = 0.0f, t = 0.0f;
   for (int i = lane; i < a.np; i += 32) {
@@ -510,97 +455,202 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
     l = warp_sum(l);
     if (lane == 0) a.loss[row] = l;
   }
-  if (a.k == 0) return;
-  // group maxima: lane l holds those of partials l, l + 32, ..., all of group l mod kp
-  float g = lane_max;
+}
+
+// One block a row, with alternatives: as head_finalize_kernel (no loss), then the k best.  The
+// chunks that reach the row's bound go to a list, 1024 chunks a round; their logits, as far as
+// they beat the k-th key known, to a buffer that is sorted and cut back to k when it fills.
+// Buffer order varies from run to run, the k largest keys do not.
+constexpr int kTopThreads = 128, kTopBuf = 512, kTopRound = 1024;
+__global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const HeadRowArgs a) {
+  griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
+  __shared__ unsigned long long buf[kTopBuf];
+  __shared__ int2 list[kTopRound];
+  __shared__ float red[4][3];
+  __shared__ int list_n, buf_n;
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int row = blockIdx.x;
+  const float4* part = a.part + static_cast<size_t>(row) * a.np;
+  float m = -INFINITY, own = -INFINITY;  // own: the largest bound of a partial's own (few rows)
+  for (int i = tid; i < a.np; i += kTopThreads) {
+    const float4 q = part[i];
+    m = fmaxf(m, q.x);
+    own = fmaxf(own, q.w);
+  }
+  // the partials' maxima in groups (i mod kp: the lane mod kp): the least group's is a bound
+  float g = m;
+  m = warp_max(m);
+  own = warp_max(own);
   for (int o = a.kp; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-  for (int o = 1; o < a.kp; o <<= 1) g = fminf(g, __shfl_xor_sync(0xffffffffu, g, o));
-  unsigned long long* buf = buf_s[w];
-  unsigned long long kth = 0;  // keys up to this one are out
-  if (ord_f32(g) > 0) kth = (static_cast<unsigned long long>(ord_f32(g)) << 32) - 1;
-  int fill = 0;
-  auto cut = [&]() {
+  __shared__ float groups[4][32];
+  groups[w][lane] = g;
+  if (lane == 0) {
+    red[w][0] = m;
+    red[w][1] = own;
+  }
+  if (tid == 0) buf_n = 0;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
+  own = fmaxf(fmaxf(red[0][1], red[1][1]), fmaxf(red[2][1], red[3][1]));
+  float low;
+  if (a.few) {
+    g = fmaxf(fmaxf(groups[0][lane], groups[1][lane]), fmaxf(groups[2][lane], groups[3][lane]));
+    for (int o = 1; o < a.kp; o <<= 1) g = fminf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    low = fmaxf(g, own);
+  } else {
+    uint32_t o = lane < a.kp ? a.bound[static_cast<size_t>(row) * a.kp + lane] : 0xffffffffu;
+    low = unord_f32(max(__reduce_min_sync(0xffffffffu, o), ord_f32(-INFINITY)));  // 0: an empty group
+  }
+  float s = 0.0f, t = 0.0f;
+  for (int i = tid; i < a.np; i += kTopThreads) {
+    const float4 q = part[i];
+    const float d = q.x - m, e = expf(d);
+    s = fmaf(q.y, e, s);
+    t = fmaf(fmaf(d, q.y, q.z), e, t);
+  }
+  s = warp_sum(s);
+  t = warp_sum(t);
+  __syncthreads();
+  if (lane == 0) {
+    red[w][0] = s;
+    red[w][1] = t;
+  }
+  __syncthreads();
+  s = (red[0][0] + red[1][0]) + (red[2][0] + red[3][0]);
+  t = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+  const float ls = logf(s);
+  if (tid == 0) {
+    a.lse_out[row] = m + ls;
+    if (a.entropy != nullptr) a.entropy[row] = ls - t / s;
+  }
+  if (tid < a.n) {
+    const size_t at = static_cast<size_t>(row) * a.n + tid;
+    const int id = a.ids[at];
+    float lp = 0.0f;
+    if (id != a.ignore) lp = id >= 0 && id < a.V ? (a.id_logit[at] - m) - ls : NAN;
+    a.logprob[at] = lp;
+  }
+
+  // ---- the alternatives: keys above kth may be among the k best
+  unsigned long long kth = ord_f32(low) > 0 ? (static_cast<unsigned long long>(ord_f32(low)) << 32) - 1 : 0;
+  const int chunks = a.np * a.cpp;
+  const float* cmax = a.cmax + static_cast<size_t>(row) * chunks;
+  const float* zrow = a.zlog + static_cast<size_t>(row) * a.V;
+  auto cut = [&](bool last) {  // all threads; buf_n keys -> the k largest, in order
+    __syncthreads();
+    const int n = buf_n;
     int size = 32;
-    while (size < fill) size <<= 1;
-    for (int i = fill + lane; i < size; i += 32) buf[i] = 0;
-    __syncwarp();
-    warp_sort_desc(buf, size, lane);
-    if (fill >= a.k) {
-      fill = a.k;
-      const unsigned long long last = buf[a.k - 1];
-      if (last > kth) kth = last;
+    while (size < n) size <<= 1;
+    for (int i = n + tid; i < size; i += kTopThreads) buf[i] = 0;
+    __syncthreads();
+    for (int kk = 2; kk <= size; kk <<= 1)
+      for (int j = kk >> 1; j > 0; j >>= 1) {
+        for (int i = tid; i < size / 2; i += kTopThreads) {
+          const int x = ((i & ~(j - 1)) << 1) | (i & (j - 1)), y = x | j;
+          const unsigned long long kx = buf[x], ky = buf[y];
+          if ((kx < ky) == ((x & kk) == 0)) {
+            buf[x] = ky;
+            buf[y] = kx;
+          }
+        }
+        __syncthreads();
+      }
+    if (n >= a.k && buf[a.k - 1] > kth) kth = buf[a.k - 1];
+    if (!last) {
+      __syncthreads();
+      if (tid == 0) buf_n = min(n, a.k);
+      __syncthreads();
     }
   };
-  for (int i0 = 0; i0 < a.np; i0 += 32) {
-    const int i = i0 + lane;
-    float4 q = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    if (i < a.np) q = part[i];
-    const int cnt = __float_as_int(q.w);
-    uint32_t have = __ballot_sync(0xffffffffu, i < a.np && cnt > 0 && q.x >= g);
-    while (have) {
-      const int src = __ffs(have) - 1;
-      have &= have - 1;
-      const int n = __shfl_sync(0xffffffffu, cnt, src);
-      unsigned long long key = 0;
-      if (lane < n) key = a.cand[(static_cast<size_t>(row) * a.np + i0 + src) * a.k + lane];
-      const uint32_t keep = __ballot_sync(0xffffffffu, key > kth);
-      if (key > kth) buf[fill + __popc(keep & ((1u << lane) - 1u))] = key;
-      fill += __popc(keep);
-      __syncwarp();
-      if (fill > kHeadBuf - 32) cut();
+  for (int q0 = 0; q0 < chunks; q0 += kTopRound) {
+    if (tid == 0) list_n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kTopRound / kTopThreads; ++u) {
+      const int q = q0 + u * kTopThreads + tid;
+      if (q < chunks) {
+        const float cm = cmax[q];
+        if (cm >= low) {
+          const int part_i = a.few ? q / a.cpp : 0;
+          const int col = a.few ? hr_first(a.V, part_i, a.np) + (q - part_i * a.cpp) * 32 : q * 32;
+          if (top_key(cm, col) > kth) list[atomicAdd(&list_n, 1)] = make_int2(q, col);
+        }
+      }
     }
+    __syncthreads();
+    const int ln = list_n;
+    for (int i0 = 0; i0 < ln;) {
+      const int room = min((kTopBuf - buf_n) / 32, ln - i0);  // chunks that fit: at least one
+      __syncthreads();
+      for (int i = i0 + w; i < i0 + room; i += 4) {
+        const int2 e = list[i];
+        const int end = a.few ? min(a.V, hr_first(a.V, e.x / a.cpp + 1, a.np)) : a.V;
+        unsigned long long key = 0;
+        if (e.y + lane < end) key = top_key(zrow[e.y + lane], e.y + lane);
+        const uint32_t keep = __ballot_sync(0xffffffffu, key > kth);
+        int base = 0;
+        if (lane == 0 && keep) base = atomicAdd(&buf_n, __popc(keep));
+        base = __shfl_sync(0xffffffffu, base, 0);
+        if (key > kth) buf[base + __popc(keep & ((1u << lane) - 1u))] = key;
+      }
+      i0 += room;
+      if (i0 < ln) cut(false);
+      else __syncthreads();
+    }
+    if (buf_n > kTopBuf - 32) cut(false);
   }
-  cut();
-  if (lane < a.k) {
-    const unsigned long long key = lane < fill ? buf[lane] : 0ull;
-    const size_t at = static_cast<size_t>(row) * a.k + lane;
+  cut(true);
+  if (tid < a.k) {
+    const unsigned long long key = tid < min(buf_n, kTopBuf) ? buf[tid] : 0ull;
+    const size_t at = static_cast<size_t>(row) * a.k + tid;
     a.top_ids[at] = key != 0 ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
     a.top_logprob[at] = key != 0 ? (unord_f32(static_cast<uint32_t>(key >> 32)) - m) - ls : NAN;
   }
 }
 
 // The backward from a saved forward, in place: e^{z-m} of a tile (fp16) becomes (bf16)
-// dz = scale·(Σ c - p·(Σc + g_H·(log p + H))) with p = e^{z-m}·e^{m-lse}.  Streams M·V bf16
-// values in and out (bound by HBM).  One warp takes 2048 columns of a row, 8 a lane and tile.
-constexpr int kHeadSpan = 8;  // tiles a warp
+// dz = scale·(Σ c - p·(Σc + g_H·(log p + H))) with p = e^{z-m}·e^{m-lse}.  Streams M·V 16-bit
+// values in and out (bound by HBM).  One warp takes 2048 columns of a row, 8 a lane and step.
+constexpr int kHeadSpan = 16;  // tiles a warp
 __global__ void __launch_bounds__(32 * kHeadRowWarps)
-    head_dlogits_saved_kernel(const HeadArgs h, int M, int V, int num_n) {
+    head_dlogits_saved_kernel(const HeadArgs h, int M, int V, int np) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
   const int lane = threadIdx.x & 31;
-  const int spans = (num_n + kHeadSpan - 1) / kHeadSpan;
+  const int spans = (np + kHeadSpan - 1) / kHeadSpan;
   const long long job = static_cast<long long>(blockIdx.x) * kHeadRowWarps + (threadIdx.x >> 5);
   const int row = static_cast<int>(job / spans);
-  const int nb0 = static_cast<int>(job % spans) * kHeadSpan;
+  const int t0 = static_cast<int>(job % spans) * kHeadSpan;
   if (row >= M) return;
   const float4 rp = h.rowp[row];
   const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
-  int pos = head_first_id(sorted, h.n, nb0 * 256);
+  int pos = head_first_id(sorted, h.n, t0 * kHeadTile);
   int2 e = pos < h.n ? sorted[pos] : make_int2(0x7fffffff, 0);
   __half* zrow = h.expz + static_cast<size_t>(row) * V;
-  const float* tm = h.tile_max + static_cast<size_t>(row) * num_n;
-  uint4 x[kHeadSpan];
-  float shift[kHeadSpan];
+  const float* tm = h.tile_max + static_cast<size_t>(row) * np;
+  constexpr int STEPS = kHeadSpan * kHeadTile / 256;
+  uint4 x[STEPS];
+  float shift[STEPS];
 #pragma unroll
-  for (int u = 0; u < kHeadSpan; ++u) {
-    const int col = (nb0 + u) * 256 + lane * 8;
+  for (int u = 0; u < STEPS; ++u) {
+    const int col = t0 * kHeadTile + u * 256 + lane * 8;
     if (col < V) x[u] = *reinterpret_cast<const uint4*>(zrow + col);
-    shift[u] = nb0 + u < num_n ? tm[nb0 + u] - rp.x : 0.0f;
+    shift[u] = col < V ? tm[col / kHeadTile] - rp.x : 0.0f;
   }
 #pragma unroll
-  for (int u = 0; u < kHeadSpan; ++u) {
-    const int col = (nb0 + u) * 256 + lane * 8;
+  for (int u = 0; u < STEPS; ++u) {
+    const int col = t0 * kHeadTile + u * 256 + lane * 8;
     const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
     float d[8];
     const float f = __expf(shift[u]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float ez = __half2float(__ushort_as_half(static_cast<unsigned short>(in[j >> 1] >> (j & 1 ? 16 : 0))));
+      const float ez = __half2float(__ushort_as_half(static_cast<unsigned short>(in[j >> 1] >> ((j & 1) ? 16 : 0))));
       const float p = ez * f;
       float wgt = rp.y;
       if (rp.z != 0.0f && ez > 0.0f) wgt = fmaf(rp.z, __logf(ez) + shift[u], wgt);
       d[j] = -h.scale * p * wgt;
     }
-    const int end = (nb0 + u) * 256 + 256;
+    const int end = t0 * kHeadTile + u * 256 + 256;
     while (e.x < end) {  // the same for every lane
       const int at = e.x - col;
 #pragma unroll

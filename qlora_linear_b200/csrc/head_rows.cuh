@@ -6,12 +6,12 @@
 // by at most 16) and walks it in tiles of up to 256 entries; X stays in L2.  Per tile the
 // tensor core computes the 128 × 256 accumulator of all rows (unused rows hold whatever shared
 // memory held; nobody reads them): half of what a CTA pair's 256 rows would cost for the same
-// bytes of W.  The statistics, the candidates and the given tokens' logits stay with the CTA
-// over its whole range, so a row leaves one partial a CTA.
+// bytes of W.  The statistics and the alternatives' bound stay with the CTA over its whole range,
+// so a row leaves one partial a CTA.
 //
 // W goes through a ring of stages of 64 of the D columns: a full tile in one TMA box of 256
-// entries, a range's last tile in boxes of 16.  The stages' number follows from what the lists
-// and X leave of shared memory (5 for one row, 3 at 128 rows with 32 alternatives).
+// entries, a range's last tile in boxes of 16.  The stages' number follows from what X leaves of
+// shared memory (6 up to 16 rows, 4 at 128).
 // Roles: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warps 2-5 epilogue (thread =
 // row).  Every wait is bounded.
 #pragma once
@@ -35,25 +35,56 @@ __host__ __device__ constexpr int hr_ctas(long long V) {
 }
 // Bytes of X in a stage: the rows rounded up to the 8-row swizzle atom.
 __host__ __device__ constexpr int hr_x_bytes(int M) { return (M + 7) / 8 * 8 * HR_BK * 2; }
-__host__ __device__ constexpr int hr_tail_bytes(int k) { return 256 + k * kHeadListThreads * 8; }
-// Stages that fit; the MMA reads 128 rows of X from any stage, so 16 KB must follow the last
-// stage's X (the tail counts towards them).
-__host__ __device__ constexpr int hr_stages(int M, int k) {
-  const int stage = HR_W_BYTES + hr_x_bytes(M);
+// Stages that fit; the MMA reads 128 rows of X from any stage, so as many must fit behind the
+// last stage's W.
+__host__ __device__ constexpr int hr_stages(int M) {
   const int behind = 128 * HR_BK * 2 - hr_x_bytes(M);
-  const int tail = hr_tail_bytes(k) > behind ? hr_tail_bytes(k) : behind;
-  const int n = (HR_SMEM_MAX - 1024 - tail) / stage;
+  const int n = (HR_SMEM_MAX - 1024 - behind) / (HR_W_BYTES + hr_x_bytes(M));
   return n < HR_MAX_STAGES ? n : HR_MAX_STAGES;
+}
+// Chunks of 32 entries of the longest range.
+__host__ __device__ constexpr int hr_chunks(long long V) {
+  return static_cast<int>((((V + 15) / 16 + hr_ctas(V) - 1) / hr_ctas(V) + 1) / 2);
 }
 
 struct HeadRowsParams {
-  HeadArgs h;              // sorted is not used; part/cand are [M][CTAs]
+  HeadArgs h;              // sorted and bound are not used; part is [M][CTAs]
+  int cpp;                 // chunks a CTA (cmax is [M][CTAs · cpp])
   const int32_t* ids;      // [M][n]
   int M, V, D;
   int stages;
   uint32_t* status;
   uint64_t wait_ns;
 };
+
+// A third look at the tile, for the alternatives: the column groups' maxima over the CTA's range
+// so far, and the least of the kp groups that they fold into.
+__device__ __forceinline__ float head_rows_bound(const HeadArgs& h, uint32_t tbase, int nv, float (&groups)[32]) {
+#pragma unroll 1
+  for (int c = 0; c * 32 < nv; ++c) {
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(tbase + c * 32, v);
+    tmem_ld_wait();
+    const int n = nv - c * 32;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < n) groups[j] = fmaxf(groups[j], __uint_as_float(v[j]) * h.scale);
+  }
+  float g[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) g[j] = groups[j];
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1)
+    if (h.kp <= s) {
+#pragma unroll
+      for (int j = 0; j < s; ++j) g[j] = fmaxf(g[j], g[j + s]);
+    }
+  float low = g[0];
+#pragma unroll
+  for (int j = 1; j < 32; ++j)
+    if (j < h.kp) low = fminf(low, g[j]);
+  return low;
+}
 
 __global__ void __launch_bounds__(HR_THREADS, 1)
     head_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -68,9 +99,8 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
   const int S = p.stages;
   const int xbytes = hr_x_bytes(p.M);
   const int stage_bytes = HR_W_BYTES + xbytes;
-  const int units = (p.V + HR_UNIT - 1) / HR_UNIT;
-  const int r0 = static_cast<int>(static_cast<long long>(units) * blockIdx.x / gridDim.x) * HR_UNIT;
-  const int r1 = static_cast<int>(static_cast<long long>(units) * (blockIdx.x + 1) / gridDim.x) * HR_UNIT;
+  const int r0 = hr_first(p.V, blockIdx.x, gridDim.x);
+  const int r1 = hr_first(p.V, blockIdx.x + 1, gridDim.x);
   const int ntiles = (r1 - r0 + HR_BN - 1) / HR_BN;
   const int nkb = (p.D + HR_BK - 1) / HR_BK;
   const WaitCtl wc{&abort_s, p.status, p.wait_ns};
@@ -175,9 +205,12 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
     const int row = quarter * 32 + lane;
     const bool in = row < p.M;
     const HeadArgs& h = p.h;
-    TopList list;
-    list.init(reinterpret_cast<unsigned long long*>(smem + S * stage_bytes) + row, h.k);
     RowStats st{-INFINITY, 0.0f, 0.0f};
+    float groups[32];  // maxima of the CTA's logits by tile column mod kp: their least is a bound
+#pragma unroll
+    for (int j = 0; j < 32; ++j) groups[j] = -INFINITY;
+    float low = -INFINITY;
+    const size_t at = static_cast<size_t>(row) * gridDim.x + blockIdx.x;
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -202,9 +235,23 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
             want &= ~__ballot_sync(0xffffffffu, col == at);
           }
         }
-        float lower;
-        const float m = head_tile_max(h, tbase, nv, in, nullptr, lower);
-        st = join_stats(st, head_tile_sums(h, tbase, nv, v0, in, m, lower, list, nullptr));
+        float cm[HR_BN / 32];
+        const float m = head_tile_max<HR_BN / 32>(tbase, nv, h.scale, cm);
+        uint32_t hits = 0;
+        if (h.k > 0) {
+          low = head_rows_bound(h, tbase, nv, groups);
+          if (in) {
+#pragma unroll
+            for (int c = 0; c < HR_BN / 32; ++c)
+              if (t * (HR_BN / 32) + c < p.cpp) {
+                h.cmax[at * p.cpp + t * (HR_BN / 32) + c] = cm[c];
+                if (c * 32 < nv && cm[c] >= low) hits |= 1u << c;
+              }
+          }
+          __syncwarp();
+        }
+        st = join_stats(st, head_tile_sums(tbase, nv, h.scale, in, m, hits,
+                                           h.zlog + static_cast<size_t>(row) * p.V + v0, nullptr));
       }
       tc_fence_before();
       __syncwarp();
@@ -212,9 +259,9 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
     if (ok && in) {
-      const size_t at = static_cast<size_t>(row) * gridDim.x + blockIdx.x;
-      h.part[at] = make_float4(st.m, st.s, st.t, __int_as_float(list.cnt));
-      for (int i = 0; i < list.cnt; ++i) h.cand[at * h.k + i] = list.s[i * kHeadListThreads];
+      h.part[at] = make_float4(st.m, st.s, st.t, low);
+      if (h.k > 0)  // a range may be a chunk shorter than the longest
+        for (int c = ntiles * (HR_BN / 32); c < p.cpp; ++c) h.cmax[at * p.cpp + c] = -INFINITY;
     }
   }
 

@@ -377,7 +377,7 @@ lora_status_t dev_info(DevInfo** out) {
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_CE_LSE>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_CE_DLOGITS>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<true, EPI_ACC_F32>), (PairCfg<true>::SMEM_BYTES));
-    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_FWD>), (PairCfg<false>::smem_bytes<EPI_HEAD_FWD>()));
+    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_FWD>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_DLOGITS>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM(head_rows_kernel, HR_SMEM_MAX);
     SET_SMEM((rowproj_kernel<16, false>), (rowproj_smem_bytes<16, false>()));
@@ -625,8 +625,8 @@ lora_status_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUte
   const int grid = static_cast<int>(2 * (pairs > 0 ? pairs : 1));
   {
     TimedRegion tr(B_MN ? LORA_KERNEL_BWD_GEMM : LORA_KERNEL_FWD_GEMM, st);
-    launch_k(lora_gemm_pair_kernel<B_MN, EPI>, dim3(grid), dim3(C::template threads<EPI>()),
-             C::template smem_bytes<EPI>(), st, a, b, e, f, p);
+    launch_k(lora_gemm_pair_kernel<B_MN, EPI>, dim3(grid), dim3(C::template threads<EPI>()), C::SMEM_BYTES, st, a, b,
+             e, f, p);
   }
   count_launch();
   return last_launch();
@@ -1188,9 +1188,10 @@ PairParams ce_params(long long M, long long Nout, long long Kred, void* out, uin
 // Rows up to which the forward without a saved buffer runs head_rows_kernel (one read of the
 // head, all rows at once) instead of the pair GEMM.
 constexpr long long kHeadFewRows = HR_ROWS;
-// Scratch the forward's per-tile results may take: the rows are worked off in chunks of a
-// multiple of 256 that keep to it (at least 256 rows).
-constexpr size_t kHeadChunkBytes = size_t(512) << 20;
+// Scratch the forward's per-tile results may take: the rows are worked off in batches of a
+// multiple of 256 that keep to it (at least 256 rows).  With alternatives a row has room for all
+// its logits, of which few are written: 2048 rows of 128256.
+constexpr size_t kHeadChunkBytes = size_t(1280) << 20;
 
 inline int pow2_at_least(int k) {
   int p = 1;
@@ -1198,20 +1199,22 @@ inline int pow2_at_least(int k) {
   return p;
 }
 
-// Forward scratch: the chunk's sorted tokens, their logits, the groups' bounds, the partials
-// of every row and tile (or CTA) and the candidates.  Pure functions of the sizes.
+// Forward scratch: the batch's sorted tokens, their logits, the bounds, the partials of every
+// row and tile (or CTA), the chunks' maxima and the logits kept.  Pure functions of the sizes.
 struct HeadFwdLayout {
   bool few = false;
   long long chunk = 0;  // rows
-  int np = 0;           // partials a row
-  size_t sorted_off = 0, logit_off = 0, bound_off = 0, part_off = 0, cand_off = 0, total = 0;
+  int np = 0, cpp = 0;  // partials a row, chunks a partial
+  size_t sorted_off = 0, logit_off = 0, bound_off = 0, part_off = 0, cmax_off = 0, zlog_off = 0, total = 0;
 };
 HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save) {
   HeadFwdLayout l;
   const int kp = k > 0 ? pow2_at_least(k) : 0;
   l.few = M <= kHeadFewRows && !save;
-  l.np = l.few ? hr_ctas(V) : cdiv(V, 256);
-  const size_t per_row = 12 * static_cast<size_t>(n) + 4 * kp + static_cast<size_t>(l.np) * (16 + 8 * static_cast<size_t>(k));
+  l.np = l.few ? hr_ctas(V) : cdiv(V, kHeadTile);
+  l.cpp = l.few ? hr_chunks(V) : kHeadTile / 32;
+  const size_t maxima = k > 0 ? static_cast<size_t>(l.np) * l.cpp * 4 : 0, logits = k > 0 ? static_cast<size_t>(V) * 4 : 0;
+  const size_t per_row = 12 * static_cast<size_t>(n) + 4 * kp + 16 * static_cast<size_t>(l.np) + maxima + logits;
   long long c = static_cast<long long>(kHeadChunkBytes / per_row) / 256 * 256;
   if (c < 256) c = 256;
   l.chunk = M < c ? M : c;
@@ -1220,8 +1223,9 @@ HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save)
   l.logit_off = l.sorted_off + align256(R * n * 8);
   l.bound_off = l.logit_off + align256(R * n * 4);
   l.part_off = l.bound_off + align256(R * kp * 4);
-  l.cand_off = l.part_off + align256(R * l.np * 16);
-  l.total = l.cand_off + align256(R * l.np * k * 8);
+  l.cmax_off = l.part_off + align256(R * l.np * 16);
+  l.zlog_off = l.cmax_off + align256(R * maxima);
+  l.total = l.zlog_off + align256(R * logits);
   return l;
 }
 
@@ -1269,6 +1273,15 @@ lora_status_t head_workspace(const void* workspace, size_t ws_bytes, size_t need
   return ws_bytes < need ? LORA_ERR_WORKSPACE : LORA_OK;
 }
 
+lora_status_t launch_head_finalize(const HeadRowArgs& r, cudaStream_t st) {
+  if (r.k > 0)
+    launch_k(head_finalize_top_kernel, dim3(r.M), dim3(kTopThreads), 0, st, r);
+  else
+    launch_k(head_finalize_kernel, dim3(cdiv(r.M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
+  count_launch();
+  return last_launch();
+}
+
 // Forward of both operators: `r` holds the caller's outputs (and, for distillation, the
 // teacher's logits) for all rows.
 lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, HeadRowArgs r, void* saved,
@@ -1291,13 +1304,17 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
   h.id_logit = reinterpret_cast<float*>(ws + l.logit_off);
   h.bound = reinterpret_cast<unsigned*>(ws + l.bound_off);
   h.part = reinterpret_cast<float4*>(ws + l.part_off);
-  h.cand = reinterpret_cast<unsigned long long*>(ws + l.cand_off);
+  h.cmax = reinterpret_cast<float*>(ws + l.cmax_off);
+  h.zlog = reinterpret_cast<float*>(ws + l.zlog_off);
   r.V = static_cast<int>(V);
   r.kp = h.kp;
   r.np = l.np;
   r.part = h.part;
   r.id_logit = h.id_logit;
-  r.cand = h.cand;
+  r.cpp = l.cpp;
+  r.few = l.few;
+  r.cmax = h.cmax;
+  r.zlog = h.zlog;
   r.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
   r.bound = k > 0 ? h.bound : nullptr;
   if (l.few) {
@@ -1307,7 +1324,8 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     p.M = static_cast<int>(M);
     p.V = static_cast<int>(V);
     p.D = static_cast<int>(D);
-    p.stages = hr_stages(p.M, k);
+    p.cpp = l.cpp;
+    p.stages = hr_stages(p.M);
     p.status = status;
     p.wait_ns = wait_limit_ns();
     CUtensorMap tx, tw, tw16;
@@ -1318,9 +1336,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     count_launch();
     TRY(last_launch());
     r.M = p.M;
-    launch_k(head_finalize_kernel, dim3(cdiv(M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
-    count_launch();
-    return last_launch();
+    return launch_head_finalize(r, st);
   }
   for (long long m0 = 0; m0 < M; m0 += l.chunk) {
     const long long m = M - m0 < l.chunk ? M - m0 : l.chunk;
@@ -1352,9 +1368,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     }
     TRY((launch_gemm_w<false, EPI_HEAD_FWD>(W, tx, tx, FSpec{Xc, static_cast<uint64_t>(D), static_cast<uint64_t>(m)}, p,
                                             dev->sms, st)));
-    launch_k(head_finalize_kernel, dim3(cdiv(m, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, a);
-    count_launch();
-    TRY(last_launch());
+    TRY(launch_head_finalize(a, st));
   }
   return LORA_OK;
 }
@@ -1364,7 +1378,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
 lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, HeadRowArgs r, void* saved, void* dX,
                             void* workspace, size_t ws_bytes, cudaStream_t st) {
   const long long V = W->N, D = W->K;
-  const int n = r.n, tiles = cdiv(V, 256);
+  const int n = r.n, tiles = cdiv(V, kHeadTile);
   // one warp of the pass over a saved buffer per row and 2048 columns
   const long long jobs = static_cast<long long>(M) * cdiv(tiles, kHeadSpan);
   if (saved && jobs > (1LL << 31) - 4) return LORA_ERR_UNSUPPORTED;
@@ -1737,7 +1751,7 @@ size_t lora_head_bwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n,
 
 size_t lora_head_saved_bytes(int64_t M, int64_t V) {
   if (M < 0 || M > (1LL << 31) - 256 || V <= 0 || V > (1LL << 30)) return 0;
-  return head_tile_max_off(M, V) + align256(static_cast<size_t>(M) * cdiv(V, 256) * 4);
+  return head_tile_max_off(M, V) + align256(static_cast<size_t>(M) * cdiv(V, kHeadTile) * 4);
 }
 
 lora_status_t lora_logprob_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,
