@@ -60,6 +60,7 @@ struct PairParams {
   int sk_on;
   int sk_dp_tiles;
   float* kpart;
+  int splits;              // EPI_HEAD_DX: every tile's fills in this many pieces (see UnitWalk)
   uint32_t* status;    // device status word, may be null
   uint64_t wait_ns;    // bound of every mbarrier wait
   // quantized weights only
@@ -84,6 +85,7 @@ enum : int {
   EPI_HEAD_FWD = 6,    // accumulator = logits / scale: per row and tile the sums, given tokens'
                        // logits and candidates of head.cuh; out is not written
   EPI_HEAD_DLOGITS = 7,  // accumulator = logits / scale: out <- scale·dz (head.cuh)
+  EPI_HEAD_DX = 8,       // out = accumulator (bf16), or with splits > 1 fp32 pieces to kpart
 };
 
 template <int EPI>
@@ -123,15 +125,20 @@ __device__ __forceinline__ void pair_tile_coords(int t, int num_m, int num_n, in
 //   remaining tiles laid end to end.  The pair's first piece goes to slot 2p, its last to
 //   slot 2p + 1 (a range inside one tile is a single piece in slot 2p); every range holds
 //   at least one fill, so the pieces of a tile are those of consecutive pairs.
+//   Splits (S > 1): unit u is piece u / ntiles of tile u mod ntiles, fills [s·L/S, (s+1)·L/S),
+//   slot u; pair p takes units p, p + P, ...  The pieces of all tiles at one depth run together,
+//   so tiles of a row or a column still share their operands in L2, which stream-K's ranges,
+//   each at a depth of its own, do not.
 struct Unit {
   int t, f0, f1, slot;
 };
 struct UnitWalk {
-  int p, P, ntiles, L, dp_left, k;
+  int p, P, ntiles, L, dp_left, k, S;
   long long g, g0, g1;
   bool sk;
-  __device__ __forceinline__ UnitWalk(int p_, int P_, int ntiles_, int L_, bool sk_, int dp_tiles)
-      : p(p_), P(P_), ntiles(ntiles_), L(L_), dp_left(sk_ ? dp_tiles / P_ : 0), k(0), g(0), g0(0), g1(0), sk(sk_) {
+  __device__ __forceinline__ UnitWalk(int p_, int P_, int ntiles_, int L_, bool sk_, int dp_tiles, int splits = 1)
+      : p(p_), P(P_), ntiles(ntiles_), L(L_), dp_left(sk_ ? dp_tiles / P_ : 0), k(0), S(splits), g(0), g0(0), g1(0),
+        sk(sk_) {
     if (sk) {
       const long long F = static_cast<long long>(ntiles - dp_tiles) * L;
       g0 = static_cast<long long>(p) * F / P;
@@ -140,6 +147,14 @@ struct UnitWalk {
     }
   }
   __device__ __forceinline__ bool next(Unit& u) {
+    if (S > 1) {
+      const int x = p + k * P, s = x / ntiles;
+      if (s >= S) return false;
+      ++k;
+      u = Unit{x - s * ntiles, static_cast<int>(static_cast<long long>(s) * L / S),
+               static_cast<int>(static_cast<long long>(s + 1) * L / S), x};
+      return true;
+    }
     if (!sk || k < dp_left) {
       const int t = p + k * P;
       if (t >= ntiles) return false;

@@ -95,6 +95,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
   const int num_n = (p.Nout + EpiTile<EPI>::COLS - 1) / EpiTile<EPI>::COLS;
   const int ntiles = num_m * num_n;
   const bool sk = EPI == EPI_STORE && p.sk_on != 0;  // only the plain store epilogue runs stream-K
+  const int splits = EPI == EPI_HEAD_DX ? p.splits : 1;
   const int nkb = (p.Kred + C::BK - 1) / C::BK;
   const int n_ext = p.r > 0 ? 1 : 0;         // one fill holds the whole LoRA block (r <= 128)
   const int tile_fills = nkb + n_ext;        // fills per tile
@@ -137,7 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       uint32_t phase = 0;
       long long fills = 0;
       bool ok = true;
-      UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles);
+      UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles, splits);
       Unit un;
       while (ok && w.next(un)) {
         int mb, nb;
@@ -216,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles);
+      UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles, splits);
       Unit un;
       while (ok && w.next(un)) {
         if (!mbar_wait<true>(smem_u32(&tempty[acc]), acc_phase ^ 1u, wc)) { ok = false; break; }
@@ -254,7 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
     const int quarter = warp & 3;  // TMEM lane quarter this warp may access
     int acc = 0;
     uint32_t acc_phase = 0;
-    UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles);
+    UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles, splits);
     Unit un;
     while (w.next(un)) {
       int mb, nb;
@@ -294,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       } else if constexpr (EPI == EPI_SWIGLU_BWD) {
         // with 8 epilogue warps, warps 2-5 and 6-9 split the 8 column chunks
         epi_swiglu_bwd_row(p, tbase, row, nb * C::BN, NEPI == 8 ? 4 * half : 0, NEPI == 8 ? 4 * half + 4 : 8);
-      } else if constexpr (EPI == EPI_STORE) {
+      } else if constexpr (EPI == EPI_STORE || EPI == EPI_HEAD_DX) {
 #pragma unroll 1
         for (int c = 0; c < C::BN / 32; ++c) {
           const int col0 = nb * C::BN + c * 32;

@@ -379,6 +379,7 @@ lora_status_t dev_info(DevInfo** out) {
     SET_SMEM((lora_gemm_pair_kernel<true, EPI_ACC_F32>), (PairCfg<true>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_FWD>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_DLOGITS>), (PairCfg<false>::SMEM_BYTES));
+    SET_SMEM((lora_gemm_pair_kernel<true, EPI_HEAD_DX>), (PairCfg<true>::SMEM_BYTES));
     SET_SMEM(head_rows_kernel, HR_SMEM_MAX);
     SET_SMEM((rowproj_kernel<16, false>), (rowproj_smem_bytes<16, false>()));
     SET_SMEM((rowproj_kernel<32, false>), (rowproj_smem_bytes<32, false>()));
@@ -621,7 +622,8 @@ lora_status_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUte
                           const PairParams& p, int sms, cudaStream_t st) {
   using C = PairCfg<B_MN>;
   const long long tiles = static_cast<long long>(cdiv(p.M, C::BM)) * cdiv(p.Nout, EpiTile<EPI>::COLS);
-  const long long pairs = p.sk_on ? kGemmPairs : (tiles < sms / 2 ? tiles : sms / 2);
+  const long long units = EPI == EPI_HEAD_DX ? tiles * p.splits : tiles;
+  const long long pairs = p.sk_on ? kGemmPairs : (units < sms / 2 ? units : sms / 2);
   const int grid = static_cast<int>(2 * (pairs > 0 ? pairs : 1));
   {
     TimedRegion tr(B_MN ? LORA_KERNEL_BWD_GEMM : LORA_KERNEL_FWD_GEMM, st);
@@ -675,7 +677,7 @@ lora_status_t launch_gemm_w(const lora_weight_t* W, const CUtensorMap& a, const 
   CUtensorMap b, f;
   TRY(tmap_bf16(&f, fs.base, fs.inner, fs.rows, kBoxX, kBoxY));
   if constexpr (EPI == EPI_CE_LSE || EPI == EPI_CE_DLOGITS || EPI == EPI_ACC_F32 || EPI == EPI_HEAD_FWD ||
-                EPI == EPI_HEAD_DLOGITS) {
+                EPI == EPI_HEAD_DLOGITS || EPI == EPI_HEAD_DX) {
     // the LM head is bf16 only (checked by the caller)
     TRY(tmap_bf16(&b, W->data, W->K, W->N, kBoxX, kBoxY));
     return launch_gemm<B_MN, EPI>(a, b, e, f, p, sms, st);
@@ -1229,8 +1231,37 @@ HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save)
   return l;
 }
 
+// Splits of the dX GEMM's reduction over the vocabulary (one wave of CTA pairs runs `pairs`
+// units, and its output has few tiles: 16 for up to 256 rows of 4096).  The cost in fills of a
+// pair: waves × (the longest piece's fills + 6 for the pipeline's start and the extra epilogue),
+// plus the pieces written and read back, 2 × 256 KB each, at the 4.3 TB/s that leaves room for
+// the operands, a fill being 0.80 us (256 × 256 × 128 at a 74th of 1.55 PFLOP/s).
+// A pure function of the sizes.  2048 rows, V = 128256, D = 4096: 128 tiles in 4 pieces, 6.92
+// waves.
+constexpr int kHeadMaxSplits = 64;
+int head_dx_splits(long long M, long long D, long long V) {
+  const long long tiles = static_cast<long long>(cdiv(M, 256)) * cdiv(D, 256);
+  const long long L = cdiv(V, 128);
+  int best = 1;
+  double best_cost = 0.0;
+  for (int s = 1; s <= kHeadMaxSplits && s <= L; ++s) {
+    const double waves = static_cast<double>((tiles * s + kGemmPairs - 1) / kGemmPairs);
+    const double slots = s > 1 ? double(tiles) * s * 2 * 262144 / 4.3e12 / 0.80e-6 + 4.0 : 0.0;
+    const double cost = waves * (static_cast<double>((L + s - 1) / s) + 6.0) + slots;
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+size_t head_dx_slot_bytes(long long M, long long D, long long V) {
+  const int s = head_dx_splits(M, D, V);
+  return s > 1 ? static_cast<size_t>(cdiv(M, 256)) * cdiv(D, 256) * s * 262144 : 0;
+}
+
 // Backward scratch: sorted (id, coefficient) pairs and row coefficients of all rows; then
-// either the stream-K slots of a dX GEMM over the whole vocabulary with, unless the logits
+// either the pieces of a dX GEMM over the whole vocabulary with, unless the logits
 // were saved, dz [M, V] behind them, or the fp32 sum of dX with a slice of dz.
 struct HeadBwdLayout {
   size_t sorted_off = 0, rowp_off = 0, slot_off = 0, whole_dz_off = 0, acc_off = 0, slice_dz_off = 0;
@@ -1240,7 +1271,7 @@ HeadBwdLayout head_bwd_layout(long long M, long long D, long long V, int n) {
   l.sorted_off = kStatusBytes;
   l.rowp_off = l.sorted_off + align256(static_cast<size_t>(M) * n * 8);
   l.slot_off = l.rowp_off + align256(static_cast<size_t>(M) * 16);
-  l.whole_dz_off = l.slot_off + align256(gemm_sched_bytes(M, D, V, 0, false));
+  l.whole_dz_off = l.slot_off + align256(head_dx_slot_bytes(M, D, V));
   l.acc_off = l.slot_off;
   l.slice_dz_off = l.acc_off + align256(static_cast<size_t>(M) * D * 4);
   return l;
@@ -1437,10 +1468,16 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
     const FSpec fs{dz, static_cast<uint64_t>(w), static_cast<uint64_t>(M)};
     PairParams q = ce_params(M, D, w, dX, status, &Wc);
     if (whole) {
-      const GemmSched g = set_sched(q, &Wc, reinterpret_cast<float*>(ws + l.slot_off), l.whole_dz_off - l.slot_off,
-                                    dev->sms);
-      TRY((launch_gemm_w<true, EPI_STORE>(&Wc, ta, ta, fs, q, dev->sms, st)));
-      TRY(streamk_fixup(q, g, st));
+      q.splits = head_dx_splits(M, D, V);
+      q.kpart = reinterpret_cast<float*>(ws + l.slot_off);
+      TRY((launch_gemm_w<true, EPI_HEAD_DX>(&Wc, ta, ta, fs, q, dev->sms, st)));
+      if (q.splits > 1) {
+        const int num_m = cdiv(M, 256), num_n = cdiv(D, 256);
+        launch_k(splits_sum_kernel, dim3(num_m * num_n, 32), dim3(256), 0, st, q.kpart, q.out, q.M, q.Nout, num_m,
+                 num_n, q.group_m, q.splits);
+        count_launch();
+        TRY(last_launch());
+      }
     } else {
       q.acc32 = reinterpret_cast<float*>(ws + l.acc_off);
       q.acc_mode = (i > 0 ? 1 : 0) | (i == nslices - 1 ? 2 : 0);

@@ -55,4 +55,27 @@ __global__ void __launch_bounds__(256) streamk_fixup_kernel(const float* __restr
       make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
 }
 
+// The second kernel of a launch with splits: out = the pieces of every tile added in order of
+// their depth.  Block (x, y): rows [8y, 8y + 8) of tile x; thread (row, 8-column chunk).
+__global__ void __launch_bounds__(256) splits_sum_kernel(const float* __restrict__ kpart, __nv_bfloat16* __restrict__ out,
+                                                         int M, int Nout, int num_m, int num_n, int group_m, int splits) {
+  griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
+  int mb, nb;
+  pair_tile_coords(blockIdx.x, num_m, num_n, group_m, mb, nb);
+  const int lr = blockIdx.y * 8 + (threadIdx.x >> 5), lc = (threadIdx.x & 31) * 8;
+  const int row = mb * 256 + lr, col = nb * 256 + lc;
+  if (row >= M || col >= Nout) return;
+  float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4* q = reinterpret_cast<const float4*>(
+        kpart + ((static_cast<size_t>(s) * gridDim.x + blockIdx.x) * 256 + lr) * 256 + lc);
+    const float4 x = q[0], y = q[1];
+    a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
+    a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+  }
+  *reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * Nout + col) =
+      make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
+}
+
 }  // namespace lora
