@@ -354,10 +354,10 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
  * W, ids and teacher_logits.  Up to 128 rows run on a kernel that reads the head once for all
  * of them.
  *
- * saved: NULL, or device memory of lora_head_saved_bytes(M, V) in which the forward keeps
- * exp(z - tile maximum) in fp16 (2·M·V bytes and a little) for the backward, which then skips
- * the logits' product, a third of the training step's work.  The backward turns the buffer
- * into dz in place: it serves one backward.  With saved == NULL the backward recomputes the
+ * saved: NULL, or device memory of lora_head_saved_bytes(M, V, n) in which the forward keeps
+ * exp(z) in bf16 (2·M·V bytes and a little; rescaled where the type could not hold it) for the
+ * backward, which then skips the logits' product, a third of the training step's work.  The
+ * backward (same n) works in that buffer: it serves one backward.  With saved == NULL the backward recomputes the
  * logits: over the whole vocabulary at once if the workspace holds dz [M, V], else slice by
  * slice, as lora_ce_bwd.
  *
@@ -374,7 +374,7 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
  */
 size_t lora_head_fwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n, int32_t k);
 size_t lora_head_bwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n, int64_t slice);
-size_t lora_head_saved_bytes(int64_t M, int64_t V);
+size_t lora_head_saved_bytes(int64_t M, int64_t V, int32_t n);
 
 lora_status_t lora_logprob_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,
                                int32_t ignore_index, float scale, int32_t k, float* logprob, float* entropy,

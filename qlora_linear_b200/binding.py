@@ -134,7 +134,7 @@ def _load() -> ctypes.CDLL:
     lib.lora_head_fwd_workspace_bytes.restype = sz
     lib.lora_head_bwd_workspace_bytes.argtypes = [i64, i64, i64, i32, i64]
     lib.lora_head_bwd_workspace_bytes.restype = sz
-    lib.lora_head_saved_bytes.argtypes = [i64, i64]
+    lib.lora_head_saved_bytes.argtypes = [i64, i64, i32]
     lib.lora_head_saved_bytes.restype = sz
     lib.lora_logprob_fwd.argtypes = [vp, i64, W, vp, i32, i32, f32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.lora_logprob_fwd.restype = i32
@@ -489,8 +489,8 @@ def head_bwd_workspace_bytes(M: int, D: int, V: int, n: int, slice_: int = 0) ->
     return int(_lib.lora_head_bwd_workspace_bytes(int(M), int(D), int(V), int(n), int(slice_)))
 
 
-def head_saved_bytes(M: int, V: int) -> int:
-    return int(_lib.lora_head_saved_bytes(int(M), int(V)))
+def head_saved_bytes(M: int, V: int, n: int) -> int:
+    return int(_lib.lora_head_saved_bytes(int(M), int(V), int(n)))
 
 
 def lora_logprob_fwd(X, M: int, W: LoraWeight, ids, n: int, ignore_index: int, scale: float, k: int, logprob, entropy,

@@ -11,15 +11,18 @@ struct HeadArgs {
   float scale;
   int n;                     // given tokens a row
   const int2* sorted;        // [M][n] by id: (id, position) forward, (id, coefficient) backward
-  float* id_logit;           // forward: [M][n]
+  float* id_logit;           // [M][n] by position; head_saved_rows_kernel: in sorted order
   int k, kp;                 // alternatives a row, and the power of two >= k of their groups
   unsigned* bound;           // forward: [M][kp] group maxima over the tiles seen so far
   float* cmax;               // forward: [M][tiles · chunks] maxima of every 32 columns
   float* zlog;               // forward: [M][V] logits of the chunks that may matter
   float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, own bound)
-  __half* expz;              // [M][V] e^{z - tile max}, or null
-  float* tile_max;           // [M][tiles], with expz
+  const uint8_t* first;      // [M][tiles of the vocabulary] tokens before each tile
+  __nv_bfloat16* expz;       // [M][V] e^{z - tau}, or null
+  float* tau;                // [M][tiles], with expz
   const float4* rowp;        // backward: [M] (lse, Σc + g_H·H, g_H, -)
+  const float* rowf;         // EPI_HEAD_DX: [M] factors of the rows, or null
+  int tiles;                 // 128-column tiles of the vocabulary
 };
 
 struct PairParams {
@@ -85,7 +88,7 @@ enum : int {
   EPI_HEAD_FWD = 6,    // accumulator = logits / scale: per row and tile the sums, given tokens'
                        // logits and candidates of head.cuh; out is not written
   EPI_HEAD_DLOGITS = 7,  // accumulator = logits / scale: out <- scale·dz (head.cuh)
-  EPI_HEAD_DX = 8,       // out = accumulator (bf16), or with splits > 1 fp32 pieces to kpart
+  EPI_HEAD_DX = 8,       // out = rowf·accumulator (bf16), or with splits > 1 fp32 pieces to kpart
 };
 
 template <int EPI>

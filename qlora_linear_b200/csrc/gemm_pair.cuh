@@ -257,25 +257,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
     uint32_t acc_phase = 0;
     UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles, splits);
     Unit un;
+    constexpr bool HEAD = EPI == EPI_HEAD_FWD || EPI == EPI_HEAD_DLOGITS;
+    auto head_pos = [&](int t) {
+      int mb, nb;
+      pair_tile_coords(t, num_m, num_n, p.group_m, mb, nb);
+      const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
+      const int col = nb * C::BN + ((warp - 2) >> 2) * kHeadTile;
+      return row < p.M && col < p.Nout
+                 ? static_cast<int>(p.head.first[static_cast<size_t>(row) * p.head.tiles + (p.v0 + col) / kHeadTile])
+                 : 0;
+    };
+    int next_pos = 0;
+    if constexpr (HEAD) {
+      if (p.head.n > 0 && pair < ntiles) next_pos = head_pos(pair);
+    }
     while (w.next(un)) {
       int mb, nb;
       pair_tile_coords(un.t, num_m, num_n, p.group_m, mb, nb);
       const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
-      // the head's epilogues: this warp's 128 columns, and the row's first given token at or
-      // above them, found while the accumulator fills
+      // the head's epilogues: this warp's 128 columns, and how many of the row's given tokens are
+      // before them, loaded a tile ahead
       const int half = NEPI == 8 ? (warp - 2) >> 2 : 0;
       const int hcol = nb * C::BN + half * kHeadTile;
-      const int2* sorted = nullptr;
-      int pos = 0;
-      int2 first = make_int2(0x7fffffff, 0);
-      float4 rowp = make_float4(0.f, 0.f, 0.f, 0.f);
-      if constexpr (EPI == EPI_HEAD_FWD || EPI == EPI_HEAD_DLOGITS) {
-        if (row < p.M) {
-          sorted = p.head.sorted + static_cast<size_t>(row) * p.head.n;
-          pos = head_first_id(sorted, p.head.n, p.v0 + hcol);
-          if (pos < p.head.n) first = sorted[pos];
-          if (EPI == EPI_HEAD_DLOGITS) rowp = p.head.rowp[row];
-        }
+      const int pos = next_pos;
+      if constexpr (HEAD) {
+        UnitWalk ahead = w;
+        Unit nx;
+        if (p.head.n > 0 && ahead.next(nx)) next_pos = head_pos(nx.t);
       }
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, wc)) break;
       tc_fence_after();
@@ -304,6 +312,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
           tmem_ld_32x32b_x32(tbase + c * 32, v);
           tmem_ld_wait();
           if (row < p.M) {
+            if (EPI == EPI_HEAD_DX && un.slot < 0 && p.head.rowf != nullptr) {
+              // a row of factor 0 is 0 whatever its operand held
+              const float f = p.head.rowf[row];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(v[j]) * f);
+            }
             if (un.slot >= 0) epi_slot_chunk<C::BM>(p, v, un.slot, row - mb * C::BM, c * 32);
             else epi_store_chunk(p, v, row, col0);
           }
@@ -383,11 +397,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       } else if constexpr (EPI == EPI_HEAD_FWD) {
         if (hcol < p.Nout)  // warp-uniform
           head_fwd_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), hcol / kHeadTile,
-                        (p.Nout + kHeadTile - 1) / kHeadTile, row < p.M, row, pos, first, p.Nout);
+                        p.head.tiles, row < p.M, row, pos, p.Nout);
       } else if constexpr (EPI == EPI_HEAD_DLOGITS) {
         if (hcol < p.Nout)  // warp-uniform
           head_dlogits_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), p.v0 + hcol, row < p.M,
-                            rowp, sorted, pos, first, p.out + static_cast<size_t>(row) * p.Nout + hcol);
+                            row, pos, p.out + static_cast<size_t>(row) * p.Nout + hcol);
       } else if constexpr (EPI == EPI_ACC_F32) {
         float* arow = p.acc32 + static_cast<size_t>(row) * p.Nout;
         __nv_bfloat16* orow = p.out + static_cast<size_t>(row) * p.Nout;

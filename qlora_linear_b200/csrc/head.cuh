@@ -60,6 +60,16 @@ __device__ __forceinline__ RowStats join_stats(const RowStats& a, const RowStats
 }
 
 // ---------------------------------------------------------------- one accumulator tile
+// The first n <= 32 logits of a chunk of accumulators (n a multiple of 8) to z.
+__device__ __forceinline__ void head_store_chunk(const uint32_t (&v)[32], int n, float scale, float* z) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q * 4 < n)
+      *reinterpret_cast<float4*>(z + q * 4) =
+          make_float4(__uint_as_float(v[4 * q]) * scale, __uint_as_float(v[4 * q + 1]) * scale,
+                      __uint_as_float(v[4 * q + 2]) * scale, __uint_as_float(v[4 * q + 3]) * scale);
+}
+
 // First pass over a row's nv <= 32·NC accumulator columns at tbase: the chunks' maxima
 // (-inf past nv), scaled.  Returns the tile's.
 template <int NC>
@@ -91,14 +101,9 @@ __device__ __forceinline__ float head_tile_max(uint32_t tbase, int nv, float sca
   return m;
 }
 
-// Second pass: the sums and, of the chunks in `hits`, the logits (zrow != null); expz != null
-// keeps e^{z-m} for the backward, in fp16: at most 1, so its 11 bits beat bf16's 8 down to
-// 2^-15, and what lies below weighs less in dX than the rounding of the tile's largest entry.
-// Full chunks run without a branch: one warp a scheduler hides the latency of exp by the
-// instructions of its other columns alone (with a test per pair of columns the pass took three
-// times as long).
-__device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float scale, bool in, float m, uint32_t hits,
-                                                   float* zrow, __half* expz) {
+// Second pass: the sums and, of the chunks in `hits`, the logits to zrow.
+__device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float scale, float m, uint32_t hits,
+                                                   float* zrow) {
   float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
 #pragma unroll 1
   for (int c = 0; c * 32 < nv; ++c) {
@@ -106,47 +111,18 @@ __device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float
     tmem_ld_32x32b_x32(tbase + c * 32, v);
     tmem_ld_wait();
     const int n = nv - c * 32;
-    if ((hits >> c) & 1u) {
+    if ((hits >> c) & 1u) head_store_chunk(v, n, scale, zrow + c * 32);
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q * 4 < n)
-          *reinterpret_cast<float4*>(zrow + c * 32 + q * 4) =
-              make_float4(__uint_as_float(v[4 * q]) * scale, __uint_as_float(v[4 * q + 1]) * scale,
-                          __uint_as_float(v[4 * q + 2]) * scale, __uint_as_float(v[4 * q + 3]) * scale);
-    }
-    if (n >= 32) {
-      float e[32];
+    for (int q = 0; q < 4; ++q)
+      if (q * 8 < n) {  // n is a multiple of 8
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float d = fmaf(__uint_as_float(v[j]), scale, -m);
-        e[j] = __expf(d);
-        s[j & 1] += e[j];
-        t[j & 1] = fmaf(d, e[j], t[j & 1]);
-      }
-      if (expz != nullptr && in) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(expz + c * 32 + q * 8) =
-              make_uint4(pack_f16x2(e[8 * q], e[8 * q + 1]), pack_f16x2(e[8 * q + 2], e[8 * q + 3]),
-                         pack_f16x2(e[8 * q + 4], e[8 * q + 5]), pack_f16x2(e[8 * q + 6], e[8 * q + 7]));
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q * 8 < n) {  // n is a multiple of 8
-          float e[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float d = fmaf(__uint_as_float(v[8 * q + j]), scale, -m);
-            e[j] = __expf(d);
-            s[j & 1] += e[j];
-            t[j & 1] = fmaf(d, e[j], t[j & 1]);
-          }
-          if (expz != nullptr && in)
-            *reinterpret_cast<uint4*>(expz + c * 32 + q * 8) = make_uint4(
-                pack_f16x2(e[0], e[1]), pack_f16x2(e[2], e[3]), pack_f16x2(e[4], e[5]), pack_f16x2(e[6], e[7]));
+        for (int j = 0; j < 8; ++j) {
+          const float d = fmaf(__uint_as_float(v[8 * q + j]), scale, -m);
+          const float e = __expf(d);
+          s[j & 1] += e;
+          t[j & 1] = fmaf(d, e, t[j & 1]);
         }
-    }
+      }
     __syncwarp();
   }
   return RowStats{m, s[0] + s[1], t[0] + t[1]};
@@ -171,37 +147,30 @@ __device__ __forceinline__ void head_tile_ids(const HeadArgs& h, uint32_t tbase,
   }
 }
 
-// First entry of the row's sorted tokens at or above v0.
-__device__ __forceinline__ int head_first_id(const int2* sorted, int n, int v0) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (sorted[mid].x < v0) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // The pair kernel's forward epilogue of one row's columns [nt·128, +128) (all lanes of the warp
-// take part).  The bound's groups are the chunks modulo kp, over every tile of the row so far,
-// in h.bound: which tiles got there first changes how many chunks are written, never the k best
-// of them.
+// take part).  The 128 logits stay in registers for both passes, so that the exponentials of all
+// columns are independent instructions: with one or two warps a scheduler nothing else hides
+// their latency (the same passes over 32 columns at a time with a test per pair of them took
+// three times as long; 350 against 130 us for 1500 rows x 65536 x 1024).  pos and the bounds
+// were loaded a tile ahead.
+//
+// The bound's groups are the chunks modulo kp, over every tile of the row so far, in h.bound:
+// which tiles got there first changes how many chunks are written, never the k best of them.
+//
+// expz != null keeps p's numerator for the backward in bf16: e^z itself, so that one factor
+// per row turns the row into probabilities and the dX GEMM can take it as it is.  A tile whose
+// maximum is below -30 or above 60 keeps e^{z - tau} with tau its maximum instead (tau 0
+// elsewhere).
 __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase, int nv, int nt, int np, bool in,
-                                              int row, int pos, int2 first, int V) {
+                                              int row, int pos, int V) {
   constexpr int NC = kHeadTile / 32;
-  float cm[NC];
-  const float m = head_tile_max<NC>(tbase, nv, h.scale, cm);
   const size_t at = static_cast<size_t>(row) * np + nt;
-  uint32_t hits = 0;
+  const size_t col0 = static_cast<size_t>(row) * V + nt * kHeadTile;
+  int2 first = make_int2(0x7fffffff, 0);
+  if (in && pos < h.n) first = h.sorted[static_cast<size_t>(row) * h.n + pos];
+  uint32_t low = 0xffffffffu;
   if (h.k > 0 && in) {
-    unsigned* bound = h.bound + static_cast<size_t>(row) * h.kp;
-    uint32_t low = 0xffffffffu;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const uint32_t o = ord_f32(cm[c]);
-      unsigned* b = bound + ((nt * NC + c) & (h.kp - 1));
-      if (o > __ldcg(b)) atomicMax(b, o);
-    }
+    const unsigned* bound = h.bound + static_cast<size_t>(row) * h.kp;
     if (h.kp >= 4) {
       for (int j = 0; j < h.kp; j += 4) {
         const uint4 b = __ldcg(reinterpret_cast<const uint4*>(bound + j));
@@ -210,26 +179,85 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
     } else {
       for (int j = 0; j < h.kp; ++j) low = min(low, __ldcg(bound + j));
     }
+  }
+  uint32_t v[NC][32];
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    if (c * 32 < nv) tmem_ld_32x32b_x32(tbase + c * 32, v[c]);  // warp-uniform
+  tmem_ld_wait();
+  if (nv < kHeadTile) {  // the vocabulary's last tile
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      if (ord_f32(cm[c]) >= low && c * 32 < nv) hits |= 1u << c;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (c * 32 + j >= nv) v[c][j] = 0xff800000u;
+  }
+  float cm[NC], m = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float a = __uint_as_float(v[c][0]), b = __uint_as_float(v[c][1]);
+#pragma unroll
+    for (int j = 2; j < 32; j += 2) {
+      a = fmaxf(a, __uint_as_float(v[c][j]));
+      b = fmaxf(b, __uint_as_float(v[c][j + 1]));
+    }
+    cm[c] = fmaxf(a, b) * h.scale;
+    m = fmaxf(m, cm[c]);
+  }
+  if (h.k > 0 && in) {
+    unsigned* bound = h.bound + static_cast<size_t>(row) * h.kp;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const uint32_t o = ord_f32(cm[c]);
+      if (o >= low) {  // cannot raise the least group otherwise
+        atomicMax(bound + ((nt * NC + c) & (h.kp - 1)), o);
+        if (c * 32 < nv) head_store_chunk(v[c], nv - c * 32, h.scale, h.zlog + col0 + c * 32);
+      }
+    }
     *reinterpret_cast<float4*>(h.cmax + at * NC) = make_float4(cm[0], cm[1], cm[2], cm[3]);
   }
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool keep = h.expz != nullptr;
+  const float tau = m < -30.0f || m > 60.0f ? m : 0.0f;
+  const float f = __expf(m - tau);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (c * 32 + q * 8 < nv) {  // warp-uniform: nv is a multiple of 8
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = fmaf(__uint_as_float(v[c][8 * q + j]), h.scale, -m);
+          e[j] = __expf(d);
+          s[j & 3] += e[j];
+          t[j & 3] = fmaf(d, e[j], t[j & 3]);
+        }
+        if (keep && in)
+          *reinterpret_cast<uint4*>(h.expz + col0 + c * 32 + q * 8) =
+              make_uint4(pack_bf16x2(e[0] * f, e[1] * f), pack_bf16x2(e[2] * f, e[3] * f),
+                         pack_bf16x2(e[4] * f, e[5] * f), pack_bf16x2(e[6] * f, e[7] * f));
+      }
+    }
+  }
   __syncwarp();
-  const size_t col0 = static_cast<size_t>(row) * V + nt * kHeadTile;
-  const RowStats st = head_tile_sums(tbase, nv, h.scale, in, m, hits, h.zlog + col0,
-                                     h.expz != nullptr ? h.expz + col0 : nullptr);
   if (h.n > 0) head_tile_ids(h, tbase, nv, nt * kHeadTile, row, pos, first);
   if (!in) return;
-  h.part[at] = make_float4(st.m, st.s, st.t, 0.0f);
-  if (h.expz != nullptr) h.tile_max[at] = st.m;
+  h.part[at] = make_float4(m, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3]), 0.0f);
+  if (keep) h.tau[at] = tau;
 }
 
 // dz of one accumulator tile of nv <= 128 columns in bf16 (recomputed logits).
 // rowp: (lse, Σc + g_H·H, g_H).
 __device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, bool in,
-                                                  const float4& rp, const int2* sorted, int pos, int2 e,
-                                                  __nv_bfloat16* orow) {
+                                                  int row, int pos, __nv_bfloat16* orow) {
+  float4 rp = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
+  int2 e = make_int2(0x7fffffff, 0);
+  if (in) {
+    rp = h.rowp[row];
+    if (pos < h.n) e = sorted[pos];
+  }
 #pragma unroll 1
   for (int c = 0; c * 32 < nv; ++c) {
     uint32_t v[32];
@@ -330,6 +358,9 @@ struct HeadRowArgs {
   float* top_logprob;      // [M][k]
   // preparation
   int2* sorted;            // [M][n]
+  uint8_t* first;          // [M][tiles + 1]: tokens before each 128-column tile
+  float* sorted_logit;     // backward from a saved forward: [M][n] id_logit in sorted order
+  float* rowf;             // backward from a saved forward: [M] see head_saved_rows_kernel
   unsigned* bound;         // [M][kp] or null
   float4* rowp;            // backward: [M]
   const float* lse;        // [M]
@@ -345,6 +376,12 @@ constexpr int kHeadRowWarps = 4;
 // 128 values in shared memory) with their position (forward) or coefficient (backward);
 // ignored and out-of-range entries go last as 0x7fffffff and match no column.  Clears the
 // forward's bounds; writes the backward's row coefficients.
+//
+// rowf (backward from a saved forward): with g_H = 0 the row's dz is -scale·C·e^{-lse} (C = Σc)
+// times the saved e^z, but for its given tokens: that factor, if lse is within what e^z can hold
+// in bf16 ([-20, 60]: the maximum is at most log V below it, and tiles beyond have their tau), C is
+// not small against Σ|c| and the factor does not underflow; 1 for rows whose dz has to be written
+// out; 0 for rows without a gradient.
 template <bool BWD>
 __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const HeadRowArgs a) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
@@ -373,9 +410,19 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
 #pragma unroll
     for (int u = 0; u < kHeadPerLane; ++u) csum += coef[u];
     csum = warp_sum(csum);
+    float cabs = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kHeadPerLane; ++u) cabs += fabsf(coef[u]);
+    cabs = warp_sum(cabs);
     if (lane == 0) {
-      const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
-      a.rowp[row] = make_float4(a.lse[row], gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh, 0.0f);
+      const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f, lse = a.lse[row];
+      a.rowp[row] = make_float4(lse, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh, 0.0f);
+      if (a.rowf != nullptr) {
+        float f = -a.scale * csum * expf(-lse);
+        if (!(gh == 0.0f && lse >= -20.0f && lse <= 60.0f && fabsf(csum) >= cabs * 0x1p-6f && fabsf(f) > 1e-30f)) f = 1.0f;
+        if (gh == 0.0f && cabs == 0.0f) f = 0.0f;
+        a.rowf[row] = f;
+      }
     }
   }
   for (int i = lane; i < a.n; i += 32) {
@@ -391,6 +438,29 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
       int before = 0;
       for (int j = 0; j < a.n; ++j) before += sid[w][j] < id || (sid[w][j] == id && j < i);
       a.sorted[static_cast<size_t>(row) * a.n + before] = make_int2(id, BWD ? __float_as_int(coef[u]) : i);
+      if (BWD && a.sorted_logit != nullptr)
+        a.sorted_logit[static_cast<size_t>(row) * a.n + before] = a.id_logit[static_cast<size_t>(row) * a.n + i];
+    }
+  }
+  __syncwarp();
+  if (a.first != nullptr) {
+    const int tiles = (a.V + kHeadTile - 1) / kHeadTile;
+    uint8_t* first = a.first + static_cast<size_t>(row) * tiles;
+    for (int t = lane; t < tiles; t += 32) {
+      int before = 0;
+      if (a.n <= 8) {
+        for (int j = 0; j < a.n; ++j) before += sid[w][j] < t * kHeadTile;
+      } else {  // sid is not sorted: count with the sorted copy
+        const int2* so = a.sorted + static_cast<size_t>(row) * a.n;
+        int lo = 0, hi = a.n;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (so[mid].x < t * kHeadTile) lo = mid + 1;
+          else hi = mid;
+        }
+        before = lo;
+      }
+      first[t] = static_cast<uint8_t>(before);
     }
   }
   if (!BWD && a.bound != nullptr && lane < a.kp) a.bound[static_cast<size_t>(row) * a.kp + lane] = 0u;
@@ -458,31 +528,44 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
 }
 
 // One block a row, with alternatives: as head_finalize_kernel (no loss), then the k best.  The
-// chunks that reach the row's bound go to a list, 1024 chunks a round; their logits, as far as
-// they beat the k-th key known, to a buffer that is sorted and cut back to k when it fills.
-// Buffer order varies from run to run, the k largest keys do not.
-constexpr int kTopThreads = 128, kTopBuf = 512, kTopRound = 1024;
+// chunks that reach the row's bound go to a list, 2048 chunks a round; their logits, as far as
+// they beat the k-th key known, to a buffer that is cut back to the k largest when it fills up
+// (usually never: about k·log k keys reach the bound).  The buffer's order varies from run to
+// run, the k largest keys do not.
+constexpr int kTopThreads = 256, kTopWarps = kTopThreads / 32, kTopBuf = 1024, kTopRound = 2048;
 __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const HeadRowArgs a) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
-  __shared__ unsigned long long buf[kTopBuf];
-  __shared__ int2 list[kTopRound];
-  __shared__ float red[4][3];
+  __shared__ unsigned long long buf[kTopBuf], top[kHeadMaxTop];
+  __shared__ int2 list[kTopRound];  // (first column, end) of a chunk
+  __shared__ float red[kTopWarps][2], groups[kTopWarps][32];
   __shared__ int list_n, buf_n;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x;
   const float4* part = a.part + static_cast<size_t>(row) * a.np;
-  float m = -INFINITY, own = -INFINITY;  // own: the largest bound of a partial's own (few rows)
-  for (int i = tid; i < a.np; i += kTopThreads) {
+  constexpr int HELD = 4;  // partials a thread keeps in registers
+  float4 held[HELD];
+  float m = -INFINITY, own = -INFINITY;  // own: the largest of the partials' own bounds (few rows)
+#pragma unroll
+  for (int u = 0; u < HELD; ++u) {
+    const int i = tid + u * kTopThreads;
+    held[u] = i < a.np ? part[i] : make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
+  }
+#pragma unroll
+  for (int u = 0; u < HELD; ++u) {
+    m = fmaxf(m, held[u].x);
+    own = fmaxf(own, held[u].w);
+  }
+  for (int i = tid + HELD * kTopThreads; i < a.np; i += kTopThreads) {
     const float4 q = part[i];
     m = fmaxf(m, q.x);
     own = fmaxf(own, q.w);
   }
-  // the partials' maxima in groups (i mod kp: the lane mod kp): the least group's is a bound
+  // few rows: the partials' maxima in groups (i mod kp: the lane mod kp); the least group's is a
+  // bound
   float g = m;
   m = warp_max(m);
   own = warp_max(own);
   for (int o = a.kp; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-  __shared__ float groups[4][32];
   groups[w][lane] = g;
   if (lane == 0) {
     red[w][0] = m;
@@ -490,24 +573,30 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   }
   if (tid == 0) buf_n = 0;
   __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-  own = fmaxf(fmaxf(red[0][1], red[1][1]), fmaxf(red[2][1], red[3][1]));
+#pragma unroll
+  for (int u = 0; u < kTopWarps; ++u) {
+    m = fmaxf(m, red[u][0]);
+    own = fmaxf(own, red[u][1]);
+    g = fmaxf(g, groups[u][lane]);
+  }
   float low;
   if (a.few) {
-    g = fmaxf(fmaxf(groups[0][lane], groups[1][lane]), fmaxf(groups[2][lane], groups[3][lane]));
     for (int o = 1; o < a.kp; o <<= 1) g = fminf(g, __shfl_xor_sync(0xffffffffu, g, o));
     low = fmaxf(g, own);
   } else {
-    uint32_t o = lane < a.kp ? a.bound[static_cast<size_t>(row) * a.kp + lane] : 0xffffffffu;
+    const uint32_t o = lane < a.kp ? a.bound[static_cast<size_t>(row) * a.kp + lane] : 0xffffffffu;
     low = unord_f32(max(__reduce_min_sync(0xffffffffu, o), ord_f32(-INFINITY)));  // 0: an empty group
   }
   float s = 0.0f, t = 0.0f;
-  for (int i = tid; i < a.np; i += kTopThreads) {
-    const float4 q = part[i];
+  auto join = [&](const float4& q) {
     const float d = q.x - m, e = expf(d);
     s = fmaf(q.y, e, s);
     t = fmaf(fmaf(d, q.y, q.z), e, t);
-  }
+  };
+#pragma unroll
+  for (int u = 0; u < HELD; ++u)
+    if (tid + u * kTopThreads < a.np) join(held[u]);
+  for (int i = tid + HELD * kTopThreads; i < a.np; i += kTopThreads) join(part[i]);
   s = warp_sum(s);
   t = warp_sum(t);
   __syncthreads();
@@ -516,8 +605,12 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     red[w][1] = t;
   }
   __syncthreads();
-  s = (red[0][0] + red[1][0]) + (red[2][0] + red[3][0]);
-  t = (red[0][1] + red[1][1]) + (red[2][1] + red[3][1]);
+  s = t = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kTopWarps; ++u) {
+    s += red[u][0];
+    t += red[u][1];
+  }
   const float ls = logf(s);
   if (tid == 0) {
     a.lse_out[row] = m + ls;
@@ -536,57 +629,54 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   const int chunks = a.np * a.cpp;
   const float* cmax = a.cmax + static_cast<size_t>(row) * chunks;
   const float* zrow = a.zlog + static_cast<size_t>(row) * a.V;
-  auto cut = [&](bool last) {  // all threads; buf_n keys -> the k largest, in order
+  auto cut = [&]() {  // all threads: the k largest of buf_n keys to top and the head of buf
     __syncthreads();
     const int n = buf_n;
-    int size = 32;
-    while (size < n) size <<= 1;
-    for (int i = n + tid; i < size; i += kTopThreads) buf[i] = 0;
+    if (tid < kHeadMaxTop) top[tid] = 0;
     __syncthreads();
-    for (int kk = 2; kk <= size; kk <<= 1)
-      for (int j = kk >> 1; j > 0; j >>= 1) {
-        for (int i = tid; i < size / 2; i += kTopThreads) {
-          const int x = ((i & ~(j - 1)) << 1) | (i & (j - 1)), y = x | j;
-          const unsigned long long kx = buf[x], ky = buf[y];
-          if ((kx < ky) == ((x & kk) == 0)) {
-            buf[x] = ky;
-            buf[y] = kx;
-          }
-        }
-        __syncthreads();
-      }
-    if (n >= a.k && buf[a.k - 1] > kth) kth = buf[a.k - 1];
-    if (!last) {
-      __syncthreads();
-      if (tid == 0) buf_n = min(n, a.k);
-      __syncthreads();
+    for (int i = tid; i < n; i += kTopThreads) {
+      const unsigned long long key = buf[i];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) rank += buf[j] > key;
+      if (rank < a.k) top[rank] = key;
     }
+    __syncthreads();
+    if (top[a.k - 1] > kth) kth = top[a.k - 1];
+    if (tid < a.k) buf[tid] = top[tid];
+    if (tid == 0) buf_n = min(n, a.k);
+    __syncthreads();
   };
   for (int q0 = 0; q0 < chunks; q0 += kTopRound) {
     if (tid == 0) list_n = 0;
     __syncthreads();
+    float cm[kTopRound / kTopThreads];
 #pragma unroll
     for (int u = 0; u < kTopRound / kTopThreads; ++u) {
       const int q = q0 + u * kTopThreads + tid;
-      if (q < chunks) {
-        const float cm = cmax[q];
-        if (cm >= low) {
-          const int part_i = a.few ? q / a.cpp : 0;
-          const int col = a.few ? hr_first(a.V, part_i, a.np) + (q - part_i * a.cpp) * 32 : q * 32;
-          if (top_key(cm, col) > kth) list[atomicAdd(&list_n, 1)] = make_int2(q, col);
+      cm[u] = q < chunks ? cmax[q] : -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < kTopRound / kTopThreads; ++u) {
+      const int q = q0 + u * kTopThreads + tid;
+      if (q < chunks && cm[u] >= low) {
+        int2 e = make_int2(q * 32, a.V);
+        if (a.few) {
+          const int i = q / a.cpp;
+          e = make_int2(hr_first(a.V, i, a.np) + (q - i * a.cpp) * 32, min(a.V, hr_first(a.V, i + 1, a.np)));
         }
+        if (top_key(cm[u], e.x) > kth) list[atomicAdd(&list_n, 1)] = e;
       }
     }
     __syncthreads();
     const int ln = list_n;
     for (int i0 = 0; i0 < ln;) {
-      const int room = min((kTopBuf - buf_n) / 32, ln - i0);  // chunks that fit: at least one
+      const int room = min((kTopBuf - buf_n) / 32, ln - i0);  // chunks that fit: 16 at least
       __syncthreads();
-      for (int i = i0 + w; i < i0 + room; i += 4) {
+      for (int i = i0 + w; i < i0 + room; i += kTopWarps) {
         const int2 e = list[i];
-        const int end = a.few ? min(a.V, hr_first(a.V, e.x / a.cpp + 1, a.np)) : a.V;
         unsigned long long key = 0;
-        if (e.y + lane < end) key = top_key(zrow[e.y + lane], e.y + lane);
+        if (e.x + lane < e.y) key = top_key(zrow[e.x + lane], e.x + lane);
         const uint32_t keep = __ballot_sync(0xffffffffu, key > kth);
         int base = 0;
         if (lane == 0 && keep) base = atomicAdd(&buf_n, __popc(keep));
@@ -594,73 +684,88 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
         if (key > kth) buf[base + __popc(keep & ((1u << lane) - 1u))] = key;
       }
       i0 += room;
-      if (i0 < ln) cut(false);
-      else __syncthreads();
+      __syncthreads();
+      if (buf_n > kTopBuf / 2) cut();
     }
-    if (buf_n > kTopBuf - 32) cut(false);
   }
-  cut(true);
+  cut();
   if (tid < a.k) {
-    const unsigned long long key = tid < min(buf_n, kTopBuf) ? buf[tid] : 0ull;
+    const unsigned long long key = top[tid];
     const size_t at = static_cast<size_t>(row) * a.k + tid;
     a.top_ids[at] = key != 0 ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
     a.top_logprob[at] = key != 0 ? (unord_f32(static_cast<uint32_t>(key >> 32)) - m) - ls : NAN;
   }
 }
 
-// The backward from a saved forward, in place: e^{z-m} of a tile (fp16) becomes (bf16)
-// dz = scale·(Σ c - p·(Σc + g_H·(log p + H))) with p = e^{z-m}·e^{m-lse}.  Streams M·V 16-bit
-// values in and out (bound by HBM).  One warp takes 2048 columns of a row, 8 a lane and step.
-constexpr int kHeadSpan = 16;  // tiles a warp
-__global__ void __launch_bounds__(32 * kHeadRowWarps)
-    head_dlogits_saved_kernel(const HeadArgs h, int M, int V, int np) {
+// The backward from a saved forward prepares the operand of the dX GEMM in place, one block a
+// row; the GEMM multiplies row m of its result by rowf[m] (head_prep_kernel).
+//   rowf = -scale·C·e^{-lse}: the saved e^z stand, but for tiles that kept e^{z-tau} (rare: times
+//     e^tau) and the given tokens, which become dz/rowf from their fp32 logits.
+//   rowf = 1 (an entropy gradient, C small against Σ|c|, an lse that e^z cannot hold): the whole
+//     row becomes dz = scale·(Σ c - p·(Σc + g_H·(log p + H))), p = e^{z-tau}·e^{tau-lse}; bound by
+//     HBM, 4·V bytes a row.
+//   rowf = 0: nothing, the GEMM's row is 0.
+constexpr int kSavedThreads = 256;
+__global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const HeadArgs h, int V, int np) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
-  const int lane = threadIdx.x & 31;
-  const int spans = (np + kHeadSpan - 1) / kHeadSpan;
-  const long long job = static_cast<long long>(blockIdx.x) * kHeadRowWarps + (threadIdx.x >> 5);
-  const int row = static_cast<int>(job / spans);
-  const int t0 = static_cast<int>(job % spans) * kHeadSpan;
-  if (row >= M) return;
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const float f = h.rowf[row];
+  if (f == 0.0f) return;
   const float4 rp = h.rowp[row];
-  const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
-  int pos = head_first_id(sorted, h.n, t0 * kHeadTile);
-  int2 e = pos < h.n ? sorted[pos] : make_int2(0x7fffffff, 0);
-  __half* zrow = h.expz + static_cast<size_t>(row) * V;
-  const float* tm = h.tile_max + static_cast<size_t>(row) * np;
-  constexpr int STEPS = kHeadSpan * kHeadTile / 256;
-  uint4 x[STEPS];
-  float shift[STEPS];
+  __nv_bfloat16* zrow = h.expz + static_cast<size_t>(row) * V;
+  const float* tau = h.tau + static_cast<size_t>(row) * np;
+  const bool whole = f == 1.0f;
+  if (whole) {
+    constexpr int U = 4;
+    for (int c0 = tid * 8; c0 < V; c0 += kSavedThreads * 8 * U) {
+      uint4 x[U];
+      float shift[U];
 #pragma unroll
-  for (int u = 0; u < STEPS; ++u) {
-    const int col = t0 * kHeadTile + u * 256 + lane * 8;
-    if (col < V) x[u] = *reinterpret_cast<const uint4*>(zrow + col);
-    shift[u] = col < V ? tm[col / kHeadTile] - rp.x : 0.0f;
+      for (int u = 0; u < U; ++u) {
+        const int col = c0 + u * kSavedThreads * 8;
+        if (col < V) {
+          x[u] = *reinterpret_cast<const uint4*>(zrow + col);
+          shift[u] = tau[col / kHeadTile] - rp.x;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int col = c0 + u * kSavedThreads * 8;
+        if (col >= V) break;
+        const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        const float es = __expf(shift[u]);
+        float d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float ez = __uint_as_float((j & 1) ? (in[j >> 1] & 0xffff0000u) : (in[j >> 1] << 16));
+          float wgt = rp.y;
+          if (rp.z != 0.0f && ez > 0.0f) wgt = fmaf(rp.z, __logf(ez) + shift[u], wgt);
+          d[j] = -h.scale * ez * es * wgt;
+        }
+        *reinterpret_cast<uint4*>(zrow + col) = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]),
+                                                           pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7]));
+      }
+    }
+  } else {
+    for (int t = tid; t < np; t += kSavedThreads) {
+      const float tt = tau[t];
+      if (tt == 0.0f) continue;
+      const float es = expf(tt);  // tau < -30 here
+      for (int col = t * kHeadTile; col < min(V, (t + 1) * kHeadTile); ++col)
+        zrow[col] = __float2bfloat16_rn(__bfloat162float(zrow[col]) * es);
+    }
   }
-#pragma unroll
-  for (int u = 0; u < STEPS; ++u) {
-    const int col = t0 * kHeadTile + u * 256 + lane * 8;
-    const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-    float d[8];
-    const float f = __expf(shift[u]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float ez = __half2float(__ushort_as_half(static_cast<unsigned short>(in[j >> 1] >> ((j & 1) ? 16 : 0))));
-      const float p = ez * f;
-      float wgt = rp.y;
-      if (rp.z != 0.0f && ez > 0.0f) wgt = fmaf(rp.z, __logf(ez) + shift[u], wgt);
-      d[j] = -h.scale * p * wgt;
-    }
-    const int end = t0 * kHeadTile + u * 256 + 256;
-    while (e.x < end) {  // the same for every lane
-      const int at = e.x - col;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j == at) d[j] = fmaf(h.scale, __int_as_float(e.y), d[j]);
-      e = ++pos < h.n ? sorted[pos] : make_int2(0x7fffffff, 0);
-    }
-    if (col < V)
-      *reinterpret_cast<uint4*>(zrow + col) = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]),
-                                                         pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7]));
+  if (h.n == 0) return;
+  __syncthreads();
+  if (tid < h.n) {
+    const int2* so = h.sorted + static_cast<size_t>(row) * h.n;
+    const int id = so[tid].x;
+    if (id == 0x7fffffff || (tid > 0 && so[tid - 1].x == id)) return;
+    float c = 0.0f;
+    for (int i = tid; i < h.n && so[i].x == id; ++i) c += __int_as_float(so[i].y);
+    const float lp = h.id_logit[static_cast<size_t>(row) * h.n + tid] - rp.x;
+    const float dz = h.scale * (c - expf(lp) * (rp.z != 0.0f ? fmaf(rp.z, lp, rp.y) : rp.y));
+    zrow[id] = __float2bfloat16_rn(whole ? dz : dz / f);
   }
 }
 

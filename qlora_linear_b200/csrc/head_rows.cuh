@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
           }
           __syncwarp();
         }
-        st = join_stats(st, head_tile_sums(tbase, nv, h.scale, in, m, hits,
-                                           h.zlog + static_cast<size_t>(row) * p.V + v0, nullptr));
+        st = join_stats(st, head_tile_sums(tbase, nv, h.scale, m, hits,
+                                           h.zlog + static_cast<size_t>(row) * p.V + v0));
       }
       tc_fence_before();
       __syncwarp();

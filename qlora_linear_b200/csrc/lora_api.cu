@@ -1207,7 +1207,7 @@ struct HeadFwdLayout {
   bool few = false;
   long long chunk = 0;  // rows
   int np = 0, cpp = 0;  // partials a row, chunks a partial
-  size_t sorted_off = 0, logit_off = 0, bound_off = 0, part_off = 0, cmax_off = 0, zlog_off = 0, total = 0;
+  size_t sorted_off = 0, logit_off = 0, first_off = 0, bound_off = 0, part_off = 0, cmax_off = 0, zlog_off = 0, total = 0;
 };
 HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save) {
   HeadFwdLayout l;
@@ -1216,14 +1216,16 @@ HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save)
   l.np = l.few ? hr_ctas(V) : cdiv(V, kHeadTile);
   l.cpp = l.few ? hr_chunks(V) : kHeadTile / 32;
   const size_t maxima = k > 0 ? static_cast<size_t>(l.np) * l.cpp * 4 : 0, logits = k > 0 ? static_cast<size_t>(V) * 4 : 0;
-  const size_t per_row = 12 * static_cast<size_t>(n) + 4 * kp + 16 * static_cast<size_t>(l.np) + maxima + logits;
+  const size_t first = n > 0 && !l.few ? cdiv(V, kHeadTile) : 0;
+  const size_t per_row = 12 * static_cast<size_t>(n) + first + 4 * kp + 16 * static_cast<size_t>(l.np) + maxima + logits;
   long long c = static_cast<long long>(kHeadChunkBytes / per_row) / 256 * 256;
   if (c < 256) c = 256;
   l.chunk = M < c ? M : c;
   const size_t R = static_cast<size_t>(l.chunk);
   l.sorted_off = kStatusBytes;
   l.logit_off = l.sorted_off + align256(R * n * 8);
-  l.bound_off = l.logit_off + align256(R * n * 4);
+  l.first_off = l.logit_off + align256(R * n * 4);
+  l.bound_off = l.first_off + align256(R * first);
   l.part_off = l.bound_off + align256(R * kp * 4);
   l.cmax_off = l.part_off + align256(R * l.np * 16);
   l.zlog_off = l.cmax_off + align256(R * maxima);
@@ -1260,24 +1262,32 @@ size_t head_dx_slot_bytes(long long M, long long D, long long V) {
   return s > 1 ? static_cast<size_t>(cdiv(M, 256)) * cdiv(D, 256) * s * 262144 : 0;
 }
 
-// Backward scratch: sorted (id, coefficient) pairs and row coefficients of all rows; then
+// Backward scratch: sorted (id, coefficient) pairs with their logits, the tiles' first of them,
+// and the coefficients of all rows; then
 // either the pieces of a dX GEMM over the whole vocabulary with, unless the logits
 // were saved, dz [M, V] behind them, or the fp32 sum of dX with a slice of dz.
 struct HeadBwdLayout {
-  size_t sorted_off = 0, rowp_off = 0, slot_off = 0, whole_dz_off = 0, acc_off = 0, slice_dz_off = 0;
+  size_t sorted_off = 0, logit_off = 0, first_off = 0, rowp_off = 0, rowf_off = 0, slot_off = 0, whole_dz_off = 0, acc_off = 0, slice_dz_off = 0;
 };
 HeadBwdLayout head_bwd_layout(long long M, long long D, long long V, int n) {
   HeadBwdLayout l;
   l.sorted_off = kStatusBytes;
-  l.rowp_off = l.sorted_off + align256(static_cast<size_t>(M) * n * 8);
-  l.slot_off = l.rowp_off + align256(static_cast<size_t>(M) * 16);
+  l.logit_off = l.sorted_off + align256(static_cast<size_t>(M) * n * 8);
+  l.first_off = l.logit_off + align256(static_cast<size_t>(M) * n * 4);
+  l.rowp_off = l.first_off + (n > 0 ? align256(static_cast<size_t>(M) * cdiv(V, kHeadTile)) : 0);
+  l.rowf_off = l.rowp_off + align256(static_cast<size_t>(M) * 16);
+  l.slot_off = l.rowf_off + align256(static_cast<size_t>(M) * 4);
   l.whole_dz_off = l.slot_off + align256(head_dx_slot_bytes(M, D, V));
   l.acc_off = l.slot_off;
   l.slice_dz_off = l.acc_off + align256(static_cast<size_t>(M) * D * 4);
   return l;
 }
 
-inline size_t head_tile_max_off(long long M, long long V) { return align256(static_cast<size_t>(M) * V * 2); }
+// A saved forward: e^{z-tau} bf16 [M, V], tau fp32 [M, tiles], the given tokens' logits fp32 [M, n].
+inline size_t head_tau_off(long long M, long long V) { return align256(static_cast<size_t>(M) * V * 2); }
+inline size_t head_saved_logit_off(long long M, long long V) {
+  return head_tau_off(M, V) + align256(static_cast<size_t>(M) * cdiv(V, kHeadTile) * 4);
+}
 
 bool head_sizes_ok(long long M, long long D, long long V, int n, int k) {
   return M >= 0 && M <= (1LL << 31) - 256 && D > 0 && D <= (1LL << 30) && V > 0 && V <= (1LL << 30) && n >= 0 &&
@@ -1348,6 +1358,9 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
   r.zlog = h.zlog;
   r.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
   r.bound = k > 0 ? h.bound : nullptr;
+  h.tiles = cdiv(V, kHeadTile);
+  h.first = ws + l.first_off;
+  r.first = n > 0 ? ws + l.first_off : nullptr;
   if (l.few) {
     HeadRowsParams p{};
     p.h = h;
@@ -1383,6 +1396,14 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     a.loss = at(r.loss, 1);
     a.top_ids = at(r.top_ids, k);
     a.top_logprob = at(r.top_logprob, k);
+    HeadArgs hc = h;
+    if (saved) {
+      uint8_t* sv = static_cast<uint8_t*>(saved);
+      hc.expz = static_cast<__nv_bfloat16*>(saved) + static_cast<size_t>(m0) * V;
+      hc.tau = reinterpret_cast<float*>(sv + head_tau_off(M, V)) + static_cast<size_t>(m0) * l.np;
+      hc.id_logit = reinterpret_cast<float*>(sv + head_saved_logit_off(M, V)) + static_cast<size_t>(m0) * n;
+      a.id_logit = hc.id_logit;
+    }
     if (n > 0 || k > 0) {
       launch_k(head_prep_kernel<false>, dim3(cdiv(m, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, a);
       count_launch();
@@ -1391,12 +1412,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     CUtensorMap tx;
     TRY(tmap_bf16(&tx, Xc, D, m, kBoxX, kBoxY));
     PairParams p = ce_params(m, V, D, nullptr, status, W);
-    p.head = h;
-    if (saved) {
-      p.head.expz = static_cast<__half*>(saved) + static_cast<size_t>(m0) * V;
-      p.head.tile_max = reinterpret_cast<float*>(static_cast<uint8_t*>(saved) + head_tile_max_off(M, V)) +
-                        static_cast<size_t>(m0) * l.np;
-    }
+    p.head = hc;
     TRY((launch_gemm_w<false, EPI_HEAD_FWD>(W, tx, tx, FSpec{Xc, static_cast<uint64_t>(D), static_cast<uint64_t>(m)}, p,
                                             dev->sms, st)));
     TRY(launch_head_finalize(a, st));
@@ -1410,9 +1426,6 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
                             void* workspace, size_t ws_bytes, cudaStream_t st) {
   const long long V = W->N, D = W->K;
   const int n = r.n, tiles = cdiv(V, kHeadTile);
-  // one warp of the pass over a saved buffer per row and 2048 columns
-  const long long jobs = static_cast<long long>(M) * cdiv(tiles, kHeadSpan);
-  if (saved && jobs > (1LL << 31) - 4) return LORA_ERR_UNSUPPORTED;
   const HeadBwdLayout l = head_bwd_layout(M, D, V, n);
   const bool whole = saved || ws_bytes >= l.whole_dz_off + static_cast<size_t>(M) * V * 2;
   TRY(head_workspace(workspace, ws_bytes, whole ? l.whole_dz_off : l.slice_dz_off));
@@ -1431,6 +1444,14 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
   r.V = static_cast<int>(V);
   r.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
   r.rowp = reinterpret_cast<float4*>(ws + l.rowp_off);
+  uint8_t* sv = static_cast<uint8_t*>(saved);
+  if (saved) {
+    r.id_logit = reinterpret_cast<const float*>(sv + head_saved_logit_off(M, V));
+    r.sorted_logit = reinterpret_cast<float*>(ws + l.logit_off);
+    r.rowf = reinterpret_cast<float*>(ws + l.rowf_off);
+  } else if (n > 0) {
+    r.first = ws + l.first_off;
+  }
   launch_k(head_prep_kernel<true>, dim3(cdiv(M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
   count_launch();
   TRY(last_launch());
@@ -1439,6 +1460,9 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
   h.n = n;
   h.sorted = r.sorted;
   h.rowp = r.rowp;
+  h.rowf = r.rowf;
+  h.first = ws + l.first_off;
+  h.tiles = tiles;
   CUtensorMap tx;
   TRY(tmap_bf16(&tx, X, D, M, kBoxX, kBoxY));
   auto* dz = saved ? static_cast<__nv_bfloat16*>(saved)
@@ -1450,10 +1474,11 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
     Wc.N = w;
     Wc.data = static_cast<const uint8_t*>(W->data) + static_cast<size_t>(v0) * D * 2;
     if (saved) {
-      h.expz = static_cast<__half*>(saved);
-      h.tile_max = reinterpret_cast<float*>(static_cast<uint8_t*>(saved) + head_tile_max_off(M, V));
-      launch_k(head_dlogits_saved_kernel, dim3(cdiv(jobs, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, h,
-               static_cast<int>(M), static_cast<int>(V), tiles);
+      h.expz = dz;
+      h.tau = reinterpret_cast<float*>(sv + head_tau_off(M, V));
+      h.id_logit = r.sorted_logit;
+      launch_k(head_saved_rows_kernel, dim3(static_cast<unsigned>(M)), dim3(kSavedThreads), 0, st, h,
+               static_cast<int>(V), tiles);
       count_launch();
       TRY(last_launch());
     } else {
@@ -1470,11 +1495,12 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
     if (whole) {
       q.splits = head_dx_splits(M, D, V);
       q.kpart = reinterpret_cast<float*>(ws + l.slot_off);
+      q.head.rowf = r.rowf;
       TRY((launch_gemm_w<true, EPI_HEAD_DX>(&Wc, ta, ta, fs, q, dev->sms, st)));
       if (q.splits > 1) {
         const int num_m = cdiv(M, 256), num_n = cdiv(D, 256);
         launch_k(splits_sum_kernel, dim3(num_m * num_n, 32), dim3(256), 0, st, q.kpart, q.out, q.M, q.Nout, num_m,
-                 num_n, q.group_m, q.splits);
+                 num_n, q.group_m, q.splits, q.head.rowf);
         count_launch();
         TRY(last_launch());
       }
@@ -1786,9 +1812,9 @@ size_t lora_head_bwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n,
   return l.slice_dz_off + align256(static_cast<size_t>(M) * ((slice + 255) / 256 * 256) * 2);
 }
 
-size_t lora_head_saved_bytes(int64_t M, int64_t V) {
-  if (M < 0 || M > (1LL << 31) - 256 || V <= 0 || V > (1LL << 30)) return 0;
-  return head_tile_max_off(M, V) + align256(static_cast<size_t>(M) * cdiv(V, kHeadTile) * 4);
+size_t lora_head_saved_bytes(int64_t M, int64_t V, int32_t n) {
+  if (!head_sizes_ok(M, 8, V, n, 0)) return 0;
+  return head_saved_logit_off(M, V) + align256(static_cast<size_t>(M) * n * 4);
 }
 
 lora_status_t lora_logprob_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,

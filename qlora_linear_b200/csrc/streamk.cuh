@@ -56,9 +56,10 @@ __global__ void __launch_bounds__(256) streamk_fixup_kernel(const float* __restr
 }
 
 // The second kernel of a launch with splits: out = the pieces of every tile added in order of
-// their depth.  Block (x, y): rows [8y, 8y + 8) of tile x; thread (row, 8-column chunk).
+// their depth, times the row's factor (rowf may be null).  Block (x, y): rows [8y, 8y + 8) of tile x; thread (row, 8-column chunk).
 __global__ void __launch_bounds__(256) splits_sum_kernel(const float* __restrict__ kpart, __nv_bfloat16* __restrict__ out,
-                                                         int M, int Nout, int num_m, int num_n, int group_m, int splits) {
+                                                         int M, int Nout, int num_m, int num_n, int group_m, int splits,
+                                                         const float* __restrict__ rowf) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
   int mb, nb;
   pair_tile_coords(blockIdx.x, num_m, num_n, group_m, mb, nb);
@@ -73,6 +74,11 @@ __global__ void __launch_bounds__(256) splits_sum_kernel(const float* __restrict
     const float4 x = q[0], y = q[1];
     a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
     a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
+  }
+  if (rowf != nullptr) {
+    const float f = rowf[row];  // a row of factor 0 is 0 whatever its operand held
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = f == 0.0f ? 0.0f : a[j] * f;
   }
   *reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * Nout + col) =
       make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));

@@ -129,8 +129,8 @@ class _HeadLayer:
             return self.slice
         return max(256, min(self.W.N, (1 << 30) // (2 * max(M, 1)) // 256 * 256))
 
-    def _saved(self, M, device):
-        return torch.empty(_b.head_saved_bytes(M, self.W.N), dtype=torch.uint8, device=device)
+    def _saved(self, M, n, device):
+        return torch.empty(_b.head_saved_bytes(M, self.W.N, n), dtype=torch.uint8, device=device)
 
     def _bwd_workspace(self, M, n, saved, device, handle):
         nb = _b.head_bwd_workspace_bytes(M, self.W.K, self.W.N, n, 0 if saved is not None else self._slice(M))
@@ -170,7 +170,7 @@ class LoraTokenLogProbs(_HeadLayer):
                 torch.empty(M, dtype=f32, device=dev) if entropy else None,
                 torch.empty((M, k), dtype=torch.int32, device=dev) if k else None,
                 torch.empty((M, k), dtype=f32, device=dev) if k else None,
-                self._saved(M, dev) if save else None)
+                self._saved(M, n, dev) if save else None)
             ws = self._workspace(_b.head_fwd_workspace_bytes(M, self.W.K, self.W.N, n, k), dev, handle)
             _b.lora_logprob_fwd(X, M, self.W, ids, n, self.ignore_index, self.scale, k, out.logprob, out.entropy,
                                 out.lse, out.top_ids, out.top_logprob, out.saved, ws, stream=handle)
@@ -222,7 +222,7 @@ class LoraDistill(_HeadLayer):
         n = self._teacher(ids, teacher_logits, M, dev)
         with self._on(X, stream, ids, teacher_logits) as handle:
             out = DistillLoss(torch.empty(M, dtype=torch.float32, device=dev),
-                              torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, dev) if save else None)
+                              torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, n, dev) if save else None)
             ws = self._workspace(_b.head_fwd_workspace_bytes(M, self.W.K, self.W.N, n), dev, handle)
             _b.lora_distill_fwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, out.loss, out.lse,
                                 out.saved, ws, stream=handle)

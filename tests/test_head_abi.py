@@ -85,7 +85,7 @@ def test_workspace_sizes():
     assert b(300, 256, 1000, 2, 256) < b(300, 256, 1000, 2, 512)
     assert b(300, 256, 1000, 2, 1000) == b(300, 256, 1000, 2, 4096)
     assert b(300, 256, 1000, 2, -1) == 0 and b(300, 0, 1000, 2, 0) == 0
-    assert s(16384, 128256) >= 2 * 16384 * 128256 and s(-1, 8) == 0 and s(4, 0) == 0
+    assert s(16384, 128256, 1) >= 2 * 16384 * 128256 and s(-1, 8, 1) == 0 and s(4, 0, 1) == 0 and s(4, 8, 129) == 0
 
 
 def test_layer_refusals():
