@@ -6,23 +6,25 @@
 
 namespace lora {
 
-// Per-row work over an LM head (head.cuh): logits z = scale·(the GEMM's output columns).
+// Per-row work over an LM head (head.cuh): logits z = scale·(the GEMM's output columns), in
+// units of log 2 y = c2·(output columns).
 struct HeadArgs {
-  float scale;
+  float scale, c2;           // scale, scale / ln 2
   int n;                     // given tokens a row
   const int2* sorted;        // [M][n] by id: (id, position) forward, (id, coefficient) backward
-  float* id_logit;           // [M][n] by position; head_saved_rows_kernel: in sorted order
+  float* id_logit;           // accumulators of the given tokens, [M][n] by position; head_saved_rows_kernel: in sorted order
   int k, kp;                 // alternatives a row, and the power of two >= k of their groups
   unsigned* bound;           // forward: [M][kp] group maxima over the tiles seen so far
   float* cmax;               // forward: [M][tiles · chunks] maxima of every 32 columns
-  float* zlog;               // forward: [M][V] logits of the chunks that may matter
-  float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, own bound)
+  float* zlog;               // forward: [M][V] accumulators of the chunks that may matter
+  float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, few rows: own bound)
   const uint8_t* first;      // [M][tiles of the vocabulary] tokens before each tile
-  __nv_bfloat16* expz;       // [M][V] e^{z - tau}, or null
+  __nv_bfloat16* expz;       // [M][V] 2^{y - tau}, or null
   float* tau;                // [M][tiles], with expz
-  const float4* rowp;        // backward: [M] (lse, Σc + g_H·H, g_H, -)
+  const float4* rowp;        // backward: [M] (lse / ln 2, Σc + g_H·H, g_H·ln 2, -)
   const float* rowf;         // EPI_HEAD_DX: [M] factors of the rows, or null
   int tiles;                 // 128-column tiles of the vocabulary
+  int rows;                  // M
 };
 
 struct PairParams {
@@ -86,8 +88,8 @@ enum : int {
   EPI_CE_DLOGITS = 4,  // accumulator = logits: out <- dloss·(exp(z - lse) - [label == column])
   EPI_ACC_F32 = 5,     // out/acc32 <- accumulator (+ acc32), see acc_mode
   EPI_HEAD_FWD = 6,    // accumulator = logits / scale: per row and tile the sums, given tokens'
-                       // logits and candidates of head.cuh; out is not written
-  EPI_HEAD_DLOGITS = 7,  // accumulator = logits / scale: out <- scale·dz (head.cuh)
+                       // logits and candidates of head.cuh; e^z to the map of E
+  EPI_HEAD_DLOGITS = 7,  // accumulator = logits / scale: scale·dz to the map of E (head.cuh)
   EPI_HEAD_DX = 8,       // out = rowf·accumulator (bf16), or with splits > 1 fp32 pieces to kpart
 };
 

@@ -61,8 +61,17 @@ struct PairCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 8 * NUM_BARS + 16;
+  // The head's epilogues stage their output between the pipeline's stages and the barriers.
+  template <int EPI>
+  static constexpr int staging() {
+    return EPI == EPI_HEAD_FWD || EPI == EPI_HEAD_DLOGITS ? epi_warps<EPI>() * 2 * kHeadStageBytes : 0;
+  }
+  template <int EPI>
+  static constexpr int smem_bytes() {
+    return SMEM_BYTES + staging<EPI>();
+  }
   static_assert(STAGE_BYTES % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
-  static_assert(SMEM_BYTES <= 232448, "shared memory");
+  static_assert(SMEM_BYTES + 8 * 2 * kHeadStageBytes <= 232448, "shared memory");
 };
 
 template <bool B_MN, int EPI>
@@ -75,7 +84,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
   constexpr int NEPI = C::template epi_warps<EPI>();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::template staging<EPI>());
   uint64_t* full = bars;                    // leader: TMA bytes of both CTAs landed
   uint64_t* empty = bars + C::STAGES;       // both: the pair MMA finished reading the stage
   uint64_t* tfull = bars + 2 * C::STAGES;   // both: accumulator ready for the epilogue
@@ -258,37 +267,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
     UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles, splits);
     Unit un;
     constexpr bool HEAD = EPI == EPI_HEAD_FWD || EPI == EPI_HEAD_DLOGITS;
-    auto head_pos = [&](int t) {
+    const uint32_t staging = smem_u32(smem + C::STAGES * C::STAGE_BYTES) + (warp - 2) * 2 * kHeadStageBytes;
+    auto head_row = [&](int t) {  // this thread's row of tile t, or -1
       int mb, nb;
       pair_tile_coords(t, num_m, num_n, p.group_m, mb, nb);
       const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
-      const int col = nb * C::BN + ((warp - 2) >> 2) * kHeadTile;
-      return row < p.M && col < p.Nout
-                 ? static_cast<int>(p.head.first[static_cast<size_t>(row) * p.head.tiles + (p.v0 + col) / kHeadTile])
-                 : 0;
+      return row < p.M && nb * C::BN + ((warp - 2) >> 2) * kHeadTile < p.Nout ? row : -1;
+    };
+    auto head_pos = [&](int t) {
+      int mb, nb;
+      pair_tile_coords(t, num_m, num_n, p.group_m, mb, nb);
+      const int row = head_row(t);
+      const int col = p.v0 + nb * C::BN + ((warp - 2) >> 2) * kHeadTile;
+      return row >= 0 ? static_cast<int>(p.head.first[static_cast<size_t>(row) * p.head.tiles + col / kHeadTile]) : 0;
     };
     int next_pos = 0;
+    HeadFirst next_first = head_load_first(p.head, -1, 0);
     if constexpr (HEAD) {
-      if (p.head.n > 0 && pair < ntiles) next_pos = head_pos(pair);
+      if (p.head.n > 0 && pair < ntiles) {
+        next_first = head_load_first(p.head, head_row(pair), head_pos(pair));
+        if (pair + npairs < ntiles) next_pos = head_pos(pair + npairs);
+      }
     }
     while (w.next(un)) {
       int mb, nb;
       pair_tile_coords(un.t, num_m, num_n, p.group_m, mb, nb);
       const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
-      // the head's epilogues: this warp's 128 columns, and how many of the row's given tokens are
-      // before them, loaded a tile ahead
+      // the head's epilogues: this warp's 128 columns, and the first of the row's given tokens at or
+      // above them, found two tiles ahead and loaded one ahead
       const int half = NEPI == 8 ? (warp - 2) >> 2 : 0;
       const int hcol = nb * C::BN + half * kHeadTile;
-      const int pos = next_pos;
+      const HeadFirst first = next_first;
       if constexpr (HEAD) {
-        UnitWalk ahead = w;
-        Unit nx;
-        if (p.head.n > 0 && ahead.next(nx)) next_pos = head_pos(nx.t);
+        if (p.head.n > 0) {
+          UnitWalk ahead = w;
+          Unit u1, u2;
+          if (ahead.next(u1)) {
+            next_first = head_load_first(p.head, head_row(u1.t), next_pos);
+            if (ahead.next(u2)) next_pos = head_pos(u2.t);
+          }
+        }
       }
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, wc)) break;
       tc_fence_after();
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * C::BN);
+      // the accumulator may be overwritten: the head's epilogues call it once their columns are in
+      // registers, with an arrive that does not wait for the last tile's global stores
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (HEAD) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&tempty[acc]), 0));
+          else mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+        }
+      };
       if constexpr (EPI == EPI_SWIGLU_FWD) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -397,11 +430,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       } else if constexpr (EPI == EPI_HEAD_FWD) {
         if (hcol < p.Nout)  // warp-uniform
           head_fwd_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), hcol / kHeadTile,
-                        p.head.tiles, row < p.M, row, pos, p.Nout);
+                        p.head.tiles, row < p.M, row, first, p.Nout, tmE, staging, release);
+        else
+          release();
       } else if constexpr (EPI == EPI_HEAD_DLOGITS) {
         if (hcol < p.Nout)  // warp-uniform
-          head_dlogits_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), p.v0 + hcol, row < p.M,
-                            row, pos, p.out + static_cast<size_t>(row) * p.Nout + hcol);
+          head_dlogits_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), p.v0 + hcol, hcol,
+                            row < p.M, row, first, tmE, staging, release);
+        else
+          release();
       } else if constexpr (EPI == EPI_ACC_F32) {
         float* arow = p.acc32 + static_cast<size_t>(row) * p.Nout;
         __nv_bfloat16* orow = p.out + static_cast<size_t>(row) * p.Nout;
@@ -437,11 +474,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+      if constexpr (!HEAD) release();
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
+    if (HEAD && lane == 0) bulk_wait<0>();  // staged stores read shared memory
   }
 
   // ------------------------------------------------------------ teardown

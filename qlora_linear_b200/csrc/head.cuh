@@ -10,10 +10,13 @@
 // for upstream gradients c_i of lp_i and g_H of H.  Distillation over a teacher's list is the
 // case c_i = -g·q_i, g_H = 0 (q the softmax of the listed teacher logits).
 //
-// A tile (128 vocabulary entries of one row, in one thread) leaves (m, Σe, Σd·e) with
-// m = max z, d = z - m, e = e^d.  Both sums stay well conditioned: the entropy of the tile is
-// log Σe - Σd·e/Σe, a sum of non-negative terms, and tiles are joined by
-// Σe ← e^{m-M}·Σe, Σd·e ← e^{m-M}·(Σd·e + (m - M)·Σe).
+// Everything between the accumulator and the row kernels is in units of log 2: with
+// y = c·acc, c = scale/ln 2 (rounded once), e^z = 2^y costs one fma, one ex2 and the sums.  A tile
+// (128 vocabulary entries of one row, in one thread) leaves (m, Σe, Σd·e) with m = max y,
+// d = y - m, e = 2^d; d comes from one fma, so m's own rounding cancels.  Both sums stay well
+// conditioned: the entropy of the tile is log Σe - ln 2·Σd·e/Σe, a sum of non-negative terms, and
+// tiles are joined by Σe ← 2^{m-M}·Σe, Σd·e ← 2^{m-M}·(Σd·e + (m - M)·Σe).  Given tokens and
+// alternatives are kept as accumulators.
 //
 // The alternatives.  Every 32 columns (a chunk) leave their maximum, and their 32 logits only
 // if that reaches a lower bound of the row's k-th largest logit; head_finalize_top_kernel then
@@ -30,6 +33,7 @@ namespace lora {
 constexpr int kHeadMaxIds = 128;   // given tokens (or teacher entries) a row
 constexpr int kHeadMaxTop = 32;    // alternatives a row
 constexpr int kHeadTile = 128;     // columns of a partial of the pair kernel
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
 // ---------------------------------------------------------------- keys of the alternatives
 // Larger key = larger logit, and among equal logits the smaller id.  -0 counts as +0; the
@@ -46,34 +50,32 @@ __device__ __forceinline__ unsigned long long top_key(float z, int id) {
 }
 
 struct RowStats {
-  float m, s, t;  // max z, Σ e^{z-m}, Σ (z-m)·e^{z-m}
+  float m, s, t;  // max y, Σ 2^{y-m}, Σ (y-m)·2^{y-m}
 };
 // a and b joined (either may be the empty {-inf, 0, 0}).
 __device__ __forceinline__ RowStats join_stats(const RowStats& a, const RowStats& b) {
   RowStats o;
   o.m = fmaxf(a.m, b.m);
   const float da = a.m == -INFINITY ? 0.0f : a.m - o.m, db = b.m == -INFINITY ? 0.0f : b.m - o.m;
-  const float ea = __expf(da), eb = __expf(db);
+  const float ea = ex2_approx(da), eb = ex2_approx(db);
   o.s = a.s * ea + b.s * eb;
   o.t = (a.t + da * a.s) * ea + (b.t + db * b.s) * eb;
   return o;
 }
 
 // ---------------------------------------------------------------- one accumulator tile
-// The first n <= 32 logits of a chunk of accumulators (n a multiple of 8) to z.
-__device__ __forceinline__ void head_store_chunk(const uint32_t (&v)[32], int n, float scale, float* z) {
+// The first n <= 32 accumulators of a chunk (n a multiple of 8) to z.
+__device__ __forceinline__ void head_store_chunk(const uint32_t (&v)[32], int n, float* z) {
 #pragma unroll
   for (int q = 0; q < 8; ++q)
     if (q * 4 < n)
-      *reinterpret_cast<float4*>(z + q * 4) =
-          make_float4(__uint_as_float(v[4 * q]) * scale, __uint_as_float(v[4 * q + 1]) * scale,
-                      __uint_as_float(v[4 * q + 2]) * scale, __uint_as_float(v[4 * q + 3]) * scale);
+      *reinterpret_cast<uint4*>(z + q * 4) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
 }
 
 // First pass over a row's nv <= 32·NC accumulator columns at tbase: the chunks' maxima
-// (-inf past nv), scaled.  Returns the tile's.
+// (-inf past nv).  Returns the tile's.
 template <int NC>
-__device__ __forceinline__ float head_tile_max(uint32_t tbase, int nv, float scale, float (&cm)[NC]) {
+__device__ __forceinline__ float head_tile_max(uint32_t tbase, int nv, float (&cm)[NC]) {
   float m = -INFINITY;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
@@ -94,15 +96,16 @@ __device__ __forceinline__ float head_tile_max(uint32_t tbase, int nv, float sca
         a = fmaxf(a, __uint_as_float(v[j]));
         b = fmaxf(b, __uint_as_float(v[j + 1]));
       }
-      cm[c] = fmaxf(a, b) * scale;
+      cm[c] = fmaxf(a, b);
       m = fmaxf(m, cm[c]);
     }
   }
   return m;
 }
 
-// Second pass: the sums and, of the chunks in `hits`, the logits to zrow.
-__device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float scale, float m, uint32_t hits,
+// Second pass: the sums about m = c2·(the maximum) and, of the chunks in `hits`, the logits to
+// zrow.
+__device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float c2, float m, uint32_t hits,
                                                    float* zrow) {
   float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
 #pragma unroll 1
@@ -111,14 +114,14 @@ __device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float
     tmem_ld_32x32b_x32(tbase + c * 32, v);
     tmem_ld_wait();
     const int n = nv - c * 32;
-    if ((hits >> c) & 1u) head_store_chunk(v, n, scale, zrow + c * 32);
+    if ((hits >> c) & 1u) head_store_chunk(v, n, zrow + c * 32);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (q * 8 < n) {  // n is a multiple of 8
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float d = fmaf(__uint_as_float(v[8 * q + j]), scale, -m);
-          const float e = __expf(d);
+          const float d = fmaf(__uint_as_float(v[8 * q + j]), c2, -m);
+          const float e = ex2_approx(d);
           s[j & 1] += e;
           t[j & 1] = fmaf(d, e, t[j & 1]);
         }
@@ -128,46 +131,118 @@ __device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float
   return RowStats{m, s[0] + s[1], t[0] + t[1]};
 }
 
-// The logits of the row's given tokens that fall into columns [v0, v0 + nv).  sorted: the
-// row's (id, position) by id, e: the first of them at or above v0 (pos: its index).  A register
-// cannot be indexed, so the warp reads each wanted column again from TMEM.
-__device__ __forceinline__ void head_tile_ids(const HeadArgs& h, uint32_t tbase, int nv, int v0, int row, int pos,
-                                              int2 e) {
+// A row's first given token at or above a tile: its index among the sorted ones, its entry
+// (0x7fffffff where there is none) and the next one's, so that the load behind a token found is
+// not waited for.
+struct HeadFirst {
+  int pos;
+  int2 e, next;
+};
+__device__ __forceinline__ int2 head_entry(const int2* sorted, int n, int pos) {
+  return pos < n ? sorted[pos] : make_int2(0x7fffffff, 0);
+}
+__device__ __forceinline__ HeadFirst head_load_first(const HeadArgs& h, int row, int pos) {
+  HeadFirst f{pos, make_int2(0x7fffffff, 0), make_int2(0x7fffffff, 0)};
+  if (row >= 0) {
+    const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
+    f.e = head_entry(sorted, h.n, pos);
+    f.next = head_entry(sorted, h.n, pos + 1);
+  }
+  return f;
+}
+__device__ __forceinline__ void head_advance(const int2* sorted, int n, HeadFirst& f) {
+  f.e = f.next;
+  f.next = head_entry(sorted, n, ++f.pos + 1);
+}
+
+// The logits of the row's given tokens that fall into columns [v0, v0 + nv).  A register cannot be
+// indexed, so the warp reads each wanted column again from TMEM.
+__device__ __forceinline__ void head_tile_ids(const HeadArgs& h, uint32_t tbase, int nv, int v0, int row, HeadFirst f) {
   const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
   while (true) {
-    const uint32_t want = __ballot_sync(0xffffffffu, e.x < v0 + nv);
+    const uint32_t want = __ballot_sync(0xffffffffu, f.e.x < v0 + nv);
     if (!want) return;
-    const int col = __shfl_sync(0xffffffffu, e.x, __ffs(want) - 1) - v0;
-    const float z = __uint_as_float(tmem_ld_32x32b_x1(tbase + col)) * h.scale;
-    while (e.x - v0 == col) {
-      h.id_logit[static_cast<size_t>(row) * h.n + e.y] = z;
-      e = ++pos < h.n ? sorted[pos] : make_int2(0x7fffffff, 0);
+    const int col = __shfl_sync(0xffffffffu, f.e.x, __ffs(want) - 1) - v0;
+    const float z = __uint_as_float(tmem_ld_32x32b_x1(tbase + col));
+    while (f.e.x - v0 == col) {
+      h.id_logit[static_cast<size_t>(row) * h.n + f.e.y] = z;
+      head_advance(sorted, h.n, f);
     }
     __syncwarp();
   }
 }
 
+// Calls f(registers, c) for the chunks of nv <= 128 columns at tbase, the next chunk's load in
+// flight meanwhile, and release() once the last one has landed.
+template <typename F, typename Release>
+__device__ __forceinline__ void head_tile_chunks(uint32_t tbase, int nv, uint32_t (&va)[32], uint32_t (&vb)[32], F f,
+                                                 Release release) {
+  tmem_ld_32x32b_x32(tbase, va);
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < kHeadTile / 32; ++c) {
+    const bool more = c + 1 < kHeadTile / 32 && (c + 1) * 32 < nv;  // warp-uniform
+    if (more) {
+      if (c & 1) tmem_ld_32x32b_x32(tbase + (c + 1) * 32, va);
+      else tmem_ld_32x32b_x32(tbase + (c + 1) * 32, vb);
+    } else {
+      release();
+    }
+    if (c & 1) f(vb, c);
+    else f(va, c);
+    if (!more) return;
+    tmem_ld_wait();
+  }
+}
+
+// Output of the pair kernel's head epilogues.  A warp's 32 rows × 32 columns (lane: row) go through
+// one of its two staging buffers and a TMA store, in the 64-byte swizzle of the output's map: rows
+// and columns outside are not written, and L2 sees whole sectors.  (16-byte stores, a row a lane,
+// write every 32-byte sector twice: 52 us more on 1500 rows x 65536 x 1024.)  c: the chunk of the
+// tile; a tile starts on the first buffer.
+constexpr int kHeadStageBytes = 2048;
+__device__ __forceinline__ void head_store_bf16(const CUtensorMap& tm, uint32_t stage, int lane, int c,
+                                                const uint32_t (&o)[16], int x, int y) {
+  const uint32_t buf = stage + (c & 1) * kHeadStageBytes;
+  if (lane == 0) {  // the stores that last read this buffer
+    if (c == 0) bulk_wait_read<0>();
+    else bulk_wait_read<1>();
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)),
+                 "r"(o[4 * q]), "r"(o[4 * q + 1]), "r"(o[4 * q + 2]), "r"(o[4 * q + 3])
+                 : "memory");
+  fence_proxy_async_smem();  // the generic writes before the TMA store reads them
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&tm, buf, x, y);
+    bulk_commit();
+  }
+}
+
 // The pair kernel's forward epilogue of one row's columns [nt·128, +128) (all lanes of the warp
-// take part).  The 128 logits stay in registers for both passes, so that the exponentials of all
-// columns are independent instructions: with one or two warps a scheduler nothing else hides
-// their latency (the same passes over 32 columns at a time with a test per pair of them took
-// three times as long; 350 against 130 us for 1500 rows x 65536 x 1024).  pos and the bounds
-// were loaded a tile ahead.
+// take part), in two passes over TMEM.  32 columns' exponentials are independent instructions
+// without a branch, and the next 32 columns load meanwhile: with two warps a scheduler nothing else
+// hides their latency.  (All 128 columns in registers saved the second read and cost more in
+// spills; a test per pair of columns took three times as long.)  The accumulator is released
+// with the last load.
 //
 // The bound's groups are the chunks modulo kp, over every tile of the row so far, in h.bound:
 // which tiles got there first changes how many chunks are written, never the k best of them.
 //
 // expz != null keeps p's numerator for the backward in bf16: e^z itself, so that one factor
 // per row turns the row into probabilities and the dX GEMM can take it as it is.  A tile whose
-// maximum is below -30 or above 60 keeps e^{z - tau} with tau its maximum instead (tau 0
+// maximum is below 2^-43 or above 2^86 keeps 2^{y - tau} with tau its maximum instead (tau 0
 // elsewhere).
+template <typename Release>
 __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase, int nv, int nt, int np, bool in,
-                                              int row, int pos, int V) {
+                                              int row, const HeadFirst& first, int V, const CUtensorMap& tm,
+                                              uint32_t stage, Release release) {
   constexpr int NC = kHeadTile / 32;
   const size_t at = static_cast<size_t>(row) * np + nt;
   const size_t col0 = static_cast<size_t>(row) * V + nt * kHeadTile;
-  int2 first = make_int2(0x7fffffff, 0);
-  if (in && pos < h.n) first = h.sorted[static_cast<size_t>(row) * h.n + pos];
   uint32_t low = 0xffffffffu;
   if (h.k > 0 && in) {
     const unsigned* bound = h.bound + static_cast<size_t>(row) * h.kp;
@@ -180,30 +255,9 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
       for (int j = 0; j < h.kp; ++j) low = min(low, __ldcg(bound + j));
     }
   }
-  uint32_t v[NC][32];
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-    if (c * 32 < nv) tmem_ld_32x32b_x32(tbase + c * 32, v[c]);  // warp-uniform
-  tmem_ld_wait();
-  if (nv < kHeadTile) {  // the vocabulary's last tile
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (c * 32 + j >= nv) v[c][j] = 0xff800000u;
-  }
-  float cm[NC], m = -INFINITY;
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    float a = __uint_as_float(v[c][0]), b = __uint_as_float(v[c][1]);
-#pragma unroll
-    for (int j = 2; j < 32; j += 2) {
-      a = fmaxf(a, __uint_as_float(v[c][j]));
-      b = fmaxf(b, __uint_as_float(v[c][j + 1]));
-    }
-    cm[c] = fmaxf(a, b) * h.scale;
-    m = fmaxf(m, cm[c]);
-  }
+  float cm[NC];
+  float m = head_tile_max<NC>(tbase, nv, cm);
+  uint32_t hits = 0;
   if (h.k > 0 && in) {
     unsigned* bound = h.bound + static_cast<size_t>(row) * h.kp;
 #pragma unroll
@@ -211,88 +265,94 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
       const uint32_t o = ord_f32(cm[c]);
       if (o >= low) {  // cannot raise the least group otherwise
         atomicMax(bound + ((nt * NC + c) & (h.kp - 1)), o);
-        if (c * 32 < nv) head_store_chunk(v[c], nv - c * 32, h.scale, h.zlog + col0 + c * 32);
+        if (c * 32 < nv) hits |= 1u << c;
       }
     }
     *reinterpret_cast<float4*>(h.cmax + at * NC) = make_float4(cm[0], cm[1], cm[2], cm[3]);
   }
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (h.n > 0) head_tile_ids(h, tbase, nv, nt * kHeadTile, row, first);
+  __syncwarp();
+  const float raw = m;
+  m *= h.c2;
   const bool keep = h.expz != nullptr;
-  const float tau = m < -30.0f || m > 60.0f ? m : 0.0f;
-  const float f = __expf(m - tau);
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  const float tau = m < -43.0f || m > 86.0f ? m : 0.0f;
+  const float f = ex2_approx(m - tau);
+  const uint64_t c2 = pack_f32x2(h.c2, h.c2), mm = pack_f32x2(-m, -m), ff = pack_f32x2(f, f);
+  uint64_t s[4] = {0, 0, 0, 0}, t[4] = {0, 0, 0, 0};
+  const int lane = threadIdx.x & 31;
+  const bool some = row - lane < h.rows;  // warp-uniform: the warp has rows
+  uint32_t va[32], vb[32];
+  auto chunk = [&](const uint32_t (&v)[32], int c) {
+    if ((hits >> c) & 1u) head_store_chunk(v, nv - c * 32, h.zlog + col0 + c * 32);
+    uint32_t o[16];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (c * 32 + q * 8 < nv) {  // warp-uniform: nv is a multiple of 8
-        float e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = fmaf(__uint_as_float(v[c][8 * q + j]), h.scale, -m);
-          e[j] = __expf(d);
-          s[j & 3] += e[j];
-          t[j & 3] = fmaf(d, e[j], t[j & 3]);
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t d = fma_f32x2(pack_f32x2(__uint_as_float(v[8 * q + 2 * j]), __uint_as_float(v[8 * q + 2 * j + 1])),
+                                       c2, mm);
+          float d0, d1;
+          unpack_f32x2(d, d0, d1);
+          uint64_t e = pack_f32x2(ex2_approx(d0), ex2_approx(d1));
+          s[j] = add_f32x2(s[j], e);
+          t[j] = fma_f32x2(d, e, t[j]);
+          e = mul_f32x2(e, ff);
+          unpack_f32x2(e, d0, d1);
+          o[4 * q + j] = pack_bf16x2(d0, d1);
         }
-        if (keep && in)
-          *reinterpret_cast<uint4*>(h.expz + col0 + c * 32 + q * 8) =
-              make_uint4(pack_bf16x2(e[0] * f, e[1] * f), pack_bf16x2(e[2] * f, e[3] * f),
-                         pack_bf16x2(e[4] * f, e[5] * f), pack_bf16x2(e[6] * f, e[7] * f));
       }
     }
-  }
-  __syncwarp();
-  if (h.n > 0) head_tile_ids(h, tbase, nv, nt * kHeadTile, row, pos, first);
+    __syncwarp();
+    if (keep && some) head_store_bf16(tm, stage, lane, c, o, nt * kHeadTile + c * 32, row - lane);
+  };
+  head_tile_chunks(tbase, nv, va, vb, chunk, release);
   if (!in) return;
-  h.part[at] = make_float4(m, (s[0] + s[1]) + (s[2] + s[3]), (t[0] + t[1]) + (t[2] + t[3]), 0.0f);
+  float a0, a1, b0, b1;
+  unpack_f32x2(add_f32x2(add_f32x2(s[0], s[1]), add_f32x2(s[2], s[3])), a0, a1);
+  unpack_f32x2(add_f32x2(add_f32x2(t[0], t[1]), add_f32x2(t[2], t[3])), b0, b1);
+  h.part[at] = make_float4(raw, a0 + a1, b0 + b1, 0.0f);
   if (keep) h.tau[at] = tau;
 }
 
 // dz of one accumulator tile of nv <= 128 columns in bf16 (recomputed logits).
-// rowp: (lse, Σc + g_H·H, g_H).
-__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, bool in,
-                                                  int row, int pos, __nv_bfloat16* orow) {
-  float4 rp = make_float4(0.f, 0.f, 0.f, 0.f);
+// rowp: (lse / ln 2, Σc + g_H·H, g_H·ln 2); x0: the tile's first column of the output.
+template <typename Release>
+__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, int x0, bool in, int row,
+                                                  HeadFirst f, const CUtensorMap& tm, uint32_t stage,
+                                                  Release release) {
+  const int lane = threadIdx.x & 31;
+  const bool some = row - lane < h.rows;  // warp-uniform: the warp has rows
   const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
-  int2 e = make_int2(0x7fffffff, 0);
-  if (in) {
-    rp = h.rowp[row];
-    if (pos < h.n) e = sorted[pos];
-  }
-#pragma unroll 1
-  for (int c = 0; c * 32 < nv; ++c) {
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(tbase + c * 32, v);
-    tmem_ld_wait();
-    const int n = min(32, nv - c * 32);
-    if (in) {
-      float d[32];
-      if (rp.z == 0.0f) {
-        const float w = -h.scale * rp.y;
+  const float4 rp = in ? h.rowp[row] : make_float4(0.f, 0.f, 0.f, 0.f);
+  uint32_t va[32], vb[32];
+  auto chunk = [&](const uint32_t (&v)[32], int c) {
+    float d[32];
+    if (rp.z == 0.0f) {
+      const float w = -h.scale * rp.y;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) d[j] = w * __expf(fmaf(__uint_as_float(v[j]), h.scale, -rp.x));
-      } else {
+      for (int j = 0; j < 32; ++j) d[j] = w * ex2_approx(fmaf(__uint_as_float(v[j]), h.c2, -rp.x));
+    } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float lp = fmaf(__uint_as_float(v[j]), h.scale, -rp.x);
-          d[j] = -h.scale * __expf(lp) * fmaf(rp.z, lp, rp.y);
-        }
+      for (int j = 0; j < 32; ++j) {
+        const float lp = fmaf(__uint_as_float(v[j]), h.c2, -rp.x);
+        d[j] = -h.scale * ex2_approx(lp) * fmaf(rp.z, lp, rp.y);
       }
-      while (e.x < v0 + c * 32 + n) {
-        const int at = e.x - v0 - c * 32;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == at) d[j] = fmaf(h.scale, __int_as_float(e.y), d[j]);
-        e = ++pos < h.n ? sorted[pos] : make_int2(0x7fffffff, 0);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q * 8 < n)
-          *reinterpret_cast<uint4*>(orow + c * 32 + q * 8) =
-              make_uint4(pack_bf16x2(d[8 * q], d[8 * q + 1]), pack_bf16x2(d[8 * q + 2], d[8 * q + 3]),
-                         pack_bf16x2(d[8 * q + 4], d[8 * q + 5]), pack_bf16x2(d[8 * q + 6], d[8 * q + 7]));
     }
+    while (f.e.x < v0 + min(nv, c * 32 + 32)) {
+      const int at = f.e.x - v0 - c * 32;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == at) d[j] = fmaf(h.scale, __int_as_float(f.e.y), d[j]);
+      head_advance(sorted, h.n, f);
+    }
+    uint32_t o[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(d[2 * j], d[2 * j + 1]);
     __syncwarp();
-  }
+    if (some) head_store_bf16(tm, stage, lane, c, o, x0 + c * 32, row - lane);
+  };
+  head_tile_chunks(tbase, nv, va, vb, chunk, release);
 }
 
 // ---------------------------------------------------------------- row kernels
@@ -338,7 +398,7 @@ __device__ __forceinline__ bool teacher_log_softmax(const int32_t* ids, const fl
 
 struct HeadRowArgs {
   int M, V, n, ignore;
-  float scale;
+  float scale, c2;         // scale, scale / ln 2
   const int32_t* ids;      // [M][n]
   const float* teacher;    // distillation: [M][n]
   // forward
@@ -416,7 +476,7 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
     cabs = warp_sum(cabs);
     if (lane == 0) {
       const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f, lse = a.lse[row];
-      a.rowp[row] = make_float4(lse, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh, 0.0f);
+      a.rowp[row] = make_float4(lse * kLog2e, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh * kLn2, 0.0f);
       if (a.rowf != nullptr) {
         float f = -a.scale * csum * expf(-lse);
         if (!(gh == 0.0f && lse >= -20.0f && lse <= 60.0f && fabsf(csum) >= cabs * 0x1p-6f && fabsf(f) > 1e-30f)) f = 1.0f;
@@ -481,11 +541,11 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
   const float4* part = a.part + static_cast<size_t>(row) * a.np;
   float m = -INFINITY;
   for (int i = lane; i < a.np; i += 32) m = fmaxf(m, part[i].x);
-  m = warp_max(m);
+  m = warp_max(m) * a.c2;
   float s = 0.0f, t = 0.0f;
   for (int i = lane; i < a.np; i += 32) {
     const float4 q = part[i];
-    const float d = q.x - m, e = expf(d);
+    const float d = q.x * a.c2 - m, e = exp2f(d);
     s = fmaf(q.y, e, s);
     t = fmaf(fmaf(d, q.y, q.z), e, t);
   }
@@ -493,8 +553,8 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
   t = warp_sum(t);
   const float ls = logf(s);
   if (lane == 0) {
-    a.lse_out[row] = m + ls;
-    if (a.entropy != nullptr) a.entropy[row] = ls - t / s;
+    a.lse_out[row] = fmaf(m, kLn2, ls);
+    if (a.entropy != nullptr) a.entropy[row] = ls - kLn2 * (t / s);
   }
   // the given tokens: z - lse as (z - max) - log Σe, which keeps the small ones' digits
   const int32_t* ids = a.ids + static_cast<size_t>(row) * a.n;
@@ -506,7 +566,7 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
     if (i < a.n) {
       const int id = ids[i];
       if (id != a.ignore)
-        lp[u] = id >= 0 && id < a.V ? (a.id_logit[static_cast<size_t>(row) * a.n + i] - m) - ls : NAN;
+        lp[u] = id >= 0 && id < a.V ? fmaf(a.id_logit[static_cast<size_t>(row) * a.n + i], a.c2, -m) * kLn2 - ls : NAN;
       if (a.logprob != nullptr) a.logprob[static_cast<size_t>(row) * a.n + i] = lp[u];
     }
   }
@@ -563,10 +623,10 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   // few rows: the partials' maxima in groups (i mod kp: the lane mod kp); the least group's is a
   // bound
   float g = m;
-  m = warp_max(m);
-  own = warp_max(own);
   for (int o = a.kp; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
   groups[w][lane] = g;
+  m = warp_max(m);
+  own = warp_max(own);
   if (lane == 0) {
     red[w][0] = m;
     red[w][1] = own;
@@ -579,6 +639,7 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     own = fmaxf(own, red[u][1]);
     g = fmaxf(g, groups[u][lane]);
   }
+  m *= a.c2;
   float low;
   if (a.few) {
     for (int o = 1; o < a.kp; o <<= 1) g = fminf(g, __shfl_xor_sync(0xffffffffu, g, o));
@@ -589,7 +650,7 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   }
   float s = 0.0f, t = 0.0f;
   auto join = [&](const float4& q) {
-    const float d = q.x - m, e = expf(d);
+    const float d = q.x * a.c2 - m, e = exp2f(d);
     s = fmaf(q.y, e, s);
     t = fmaf(fmaf(d, q.y, q.z), e, t);
   };
@@ -613,14 +674,14 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   }
   const float ls = logf(s);
   if (tid == 0) {
-    a.lse_out[row] = m + ls;
-    if (a.entropy != nullptr) a.entropy[row] = ls - t / s;
+    a.lse_out[row] = fmaf(m, kLn2, ls);
+    if (a.entropy != nullptr) a.entropy[row] = ls - kLn2 * (t / s);
   }
   if (tid < a.n) {
     const size_t at = static_cast<size_t>(row) * a.n + tid;
     const int id = a.ids[at];
     float lp = 0.0f;
-    if (id != a.ignore) lp = id >= 0 && id < a.V ? (a.id_logit[at] - m) - ls : NAN;
+    if (id != a.ignore) lp = id >= 0 && id < a.V ? fmaf(a.id_logit[at], a.c2, -m) * kLn2 - ls : NAN;
     a.logprob[at] = lp;
   }
 
@@ -693,17 +754,16 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     const unsigned long long key = top[tid];
     const size_t at = static_cast<size_t>(row) * a.k + tid;
     a.top_ids[at] = key != 0 ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
-    a.top_logprob[at] = key != 0 ? (unord_f32(static_cast<uint32_t>(key >> 32)) - m) - ls : NAN;
+    a.top_logprob[at] = key != 0 ? fmaf(unord_f32(static_cast<uint32_t>(key >> 32)), a.c2, -m) * kLn2 - ls : NAN;
   }
 }
 
 // The backward from a saved forward prepares the operand of the dX GEMM in place, one block a
 // row; the GEMM multiplies row m of its result by rowf[m] (head_prep_kernel).
-//   rowf = -scale·C·e^{-lse}: the saved e^z stand, but for tiles that kept e^{z-tau} (rare: times
-//     e^tau) and the given tokens, which become dz/rowf from their fp32 logits.
+//   rowf = -scale·C·e^{-lse}: the saved e^z stand, but for tiles that kept 2^{y-tau} (rare: times
+//     2^tau) and the given tokens, which become dz/rowf from their fp32 logits.
 //   rowf = 1 (an entropy gradient, C small against Σ|c|, an lse that e^z cannot hold): the whole
-//     row becomes dz = scale·(Σ c - p·(Σc + g_H·(log p + H))), p = e^{z-tau}·e^{tau-lse}; bound by
-//     HBM, 4·V bytes a row.
+//     row becomes dz = scale·(Σ c - p·(Σc + g_H·(log p + H))); bound by HBM, 4·V bytes a row.
 //   rowf = 0: nothing, the GEMM's row is 0.
 constexpr int kSavedThreads = 256;
 __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const HeadArgs h, int V, int np) {
@@ -733,13 +793,13 @@ __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const He
         const int col = c0 + u * kSavedThreads * 8;
         if (col >= V) break;
         const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        const float es = __expf(shift[u]);
+        const float es = ex2_approx(shift[u]);
         float d[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float ez = __uint_as_float((j & 1) ? (in[j >> 1] & 0xffff0000u) : (in[j >> 1] << 16));
           float wgt = rp.y;
-          if (rp.z != 0.0f && ez > 0.0f) wgt = fmaf(rp.z, __logf(ez) + shift[u], wgt);
+          if (rp.z != 0.0f && ez > 0.0f) wgt = fmaf(rp.z, lg2_approx(ez) + shift[u], wgt);
           d[j] = -h.scale * ez * es * wgt;
         }
         *reinterpret_cast<uint4*>(zrow + col) = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]),
@@ -750,7 +810,7 @@ __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const He
     for (int t = tid; t < np; t += kSavedThreads) {
       const float tt = tau[t];
       if (tt == 0.0f) continue;
-      const float es = expf(tt);  // tau < -30 here
+      const float es = exp2f(tt);  // tau < -43 here
       for (int col = t * kHeadTile; col < min(V, (t + 1) * kHeadTile); ++col)
         zrow[col] = __float2bfloat16_rn(__bfloat162float(zrow[col]) * es);
     }
@@ -763,8 +823,8 @@ __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const He
     if (id == 0x7fffffff || (tid > 0 && so[tid - 1].x == id)) return;
     float c = 0.0f;
     for (int i = tid; i < h.n && so[i].x == id; ++i) c += __int_as_float(so[i].y);
-    const float lp = h.id_logit[static_cast<size_t>(row) * h.n + tid] - rp.x;
-    const float dz = h.scale * (c - expf(lp) * (rp.z != 0.0f ? fmaf(rp.z, lp, rp.y) : rp.y));
+    const float lp = fmaf(h.id_logit[static_cast<size_t>(row) * h.n + tid], h.c2, -rp.x);
+    const float dz = h.scale * (c - exp2f(lp) * (rp.z != 0.0f ? fmaf(rp.z, lp, rp.y) : rp.y));
     zrow[id] = __float2bfloat16_rn(whole ? dz : dz / f);
   }
 }

@@ -68,7 +68,7 @@ __device__ __forceinline__ float head_rows_bound(const HeadArgs& h, uint32_t tba
     const int n = nv - c * 32;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (j < n) groups[j] = fmaxf(groups[j], __uint_as_float(v[j]) * h.scale);
+      if (j < n) groups[j] = fmaxf(groups[j], __uint_as_float(v[j]));
   }
   float g[32];
 #pragma unroll
@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
     const bool in = row < p.M;
     const HeadArgs& h = p.h;
     RowStats st{-INFINITY, 0.0f, 0.0f};
+    float raw = -INFINITY;  // the largest accumulator (st.m in units of log 2)
     float groups[32];  // maxima of the CTA's logits by tile column mod kp: their least is a bound
 #pragma unroll
     for (int j = 0; j < 32; ++j) groups[j] = -INFINITY;
@@ -230,13 +231,14 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
           uint32_t want = __ballot_sync(0xffffffffu, col >= 0);
           while (want) {
             const int at = __shfl_sync(0xffffffffu, col, __ffs(want) - 1);
-            const float z = __uint_as_float(tmem_ld_32x32b_x1(tbase + at)) * h.scale;
+            const float z = __uint_as_float(tmem_ld_32x32b_x1(tbase + at));
             if (col == at) h.id_logit[static_cast<size_t>(row) * h.n + i] = z;
             want &= ~__ballot_sync(0xffffffffu, col == at);
           }
         }
         float cm[HR_BN / 32];
-        const float m = head_tile_max<HR_BN / 32>(tbase, nv, h.scale, cm);
+        const float tile_max = head_tile_max<HR_BN / 32>(tbase, nv, cm), m = tile_max * h.c2;
+        raw = fmaxf(raw, tile_max);
         uint32_t hits = 0;
         if (h.k > 0) {
           low = head_rows_bound(h, tbase, nv, groups);
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
           }
           __syncwarp();
         }
-        st = join_stats(st, head_tile_sums(tbase, nv, h.scale, m, hits,
+        st = join_stats(st, head_tile_sums(tbase, nv, h.c2, m, hits,
                                            h.zlog + static_cast<size_t>(row) * p.V + v0));
       }
       tc_fence_before();
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
     if (ok && in) {
-      h.part[at] = make_float4(st.m, st.s, st.t, low);
+      h.part[at] = make_float4(raw, st.s, st.t, low);
       if (h.k > 0)  // a range may be a chunk shorter than the longest
         for (int c = ntiles * (HR_BN / 32); c < p.cpp; ++c) h.cmax[at * p.cpp + c] = -INFINITY;
     }

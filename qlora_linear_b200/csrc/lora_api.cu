@@ -377,8 +377,8 @@ lora_status_t dev_info(DevInfo** out) {
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_CE_LSE>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<false, EPI_CE_DLOGITS>), (PairCfg<false>::SMEM_BYTES));
     SET_SMEM((lora_gemm_pair_kernel<true, EPI_ACC_F32>), (PairCfg<true>::SMEM_BYTES));
-    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_FWD>), (PairCfg<false>::SMEM_BYTES));
-    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_DLOGITS>), (PairCfg<false>::SMEM_BYTES));
+    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_FWD>), (PairCfg<false>::smem_bytes<EPI_HEAD_FWD>()));
+    SET_SMEM((lora_gemm_pair_kernel<false, EPI_HEAD_DLOGITS>), (PairCfg<false>::smem_bytes<EPI_HEAD_DLOGITS>()));
     SET_SMEM((lora_gemm_pair_kernel<true, EPI_HEAD_DX>), (PairCfg<true>::SMEM_BYTES));
     SET_SMEM(head_rows_kernel, HR_SMEM_MAX);
     SET_SMEM((rowproj_kernel<16, false>), (rowproj_smem_bytes<16, false>()));
@@ -439,6 +439,11 @@ lora_status_t tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int elem_bytes, co
 }
 lora_status_t tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t bi, uint32_t br) {
   return tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, rows, bi, br, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// The map of a bf16 output written through 32 × 32 staging buffers.
+lora_status_t tmap_staged(CUtensorMap* m, void* base, uint64_t inner, uint64_t rows) {
+  return tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // ---------------------------------------------------------------- validation
@@ -627,8 +632,8 @@ lora_status_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUte
   const int grid = static_cast<int>(2 * (pairs > 0 ? pairs : 1));
   {
     TimedRegion tr(B_MN ? LORA_KERNEL_BWD_GEMM : LORA_KERNEL_FWD_GEMM, st);
-    launch_k(lora_gemm_pair_kernel<B_MN, EPI>, dim3(grid), dim3(C::template threads<EPI>()), C::SMEM_BYTES, st, a, b,
-             e, f, p);
+    launch_k(lora_gemm_pair_kernel<B_MN, EPI>, dim3(grid), dim3(C::template threads<EPI>()),
+             C::template smem_bytes<EPI>(), st, a, b, e, f, p);
   }
   count_launch();
   return last_launch();
@@ -1338,6 +1343,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   HeadArgs h{};
   h.scale = r.scale;
+  h.c2 = r.c2 = static_cast<float>(static_cast<double>(r.scale) * 1.4426950408889634);
   h.n = n;
   h.k = k;
   h.kp = k > 0 ? pow2_at_least(k) : 0;
@@ -1413,7 +1419,10 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     TRY(tmap_bf16(&tx, Xc, D, m, kBoxX, kBoxY));
     PairParams p = ce_params(m, V, D, nullptr, status, W);
     p.head = hc;
-    TRY((launch_gemm_w<false, EPI_HEAD_FWD>(W, tx, tx, FSpec{Xc, static_cast<uint64_t>(D), static_cast<uint64_t>(m)}, p,
+    p.head.rows = p.M;
+    CUtensorMap te = tx;  // not used unless e^z is kept
+    if (saved) TRY(tmap_staged(&te, hc.expz, V, m));
+    TRY((launch_gemm_w<false, EPI_HEAD_FWD>(W, tx, te, FSpec{Xc, static_cast<uint64_t>(D), static_cast<uint64_t>(m)}, p,
                                             dev->sms, st)));
     TRY(launch_head_finalize(a, st));
   }
@@ -1457,6 +1466,7 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
   TRY(last_launch());
   HeadArgs h{};
   h.scale = r.scale;
+  h.c2 = r.c2 = static_cast<float>(static_cast<double>(r.scale) * 1.4426950408889634);
   h.n = n;
   h.sorted = r.sorted;
   h.rowp = r.rowp;
@@ -1485,8 +1495,11 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
       PairParams p = ce_params(M, w, D, dz, status, &Wc);
       p.v0 = static_cast<int>(v0);
       p.head = h;
+      p.head.rows = p.M;
+      CUtensorMap te;
+      TRY(tmap_staged(&te, dz, w, M));
       TRY((launch_gemm_w<false, EPI_HEAD_DLOGITS>(
-          &Wc, tx, tx, FSpec{X, static_cast<uint64_t>(D), static_cast<uint64_t>(M)}, p, dev->sms, st)));
+          &Wc, tx, te, FSpec{X, static_cast<uint64_t>(D), static_cast<uint64_t>(M)}, p, dev->sms, st)));
     }
     CUtensorMap ta;
     TRY(tmap_bf16(&ta, dz, w, M, kBoxX, kBoxY));
