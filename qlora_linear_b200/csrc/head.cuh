@@ -96,7 +96,7 @@ __device__ __forceinline__ float head_tile_max(uint32_t tbase, int nv, float (&c
         a = fmaxf(a, __uint_as_float(v[j]));
         b = fmaxf(b, __uint_as_float(v[j + 1]));
       }
-      cm[c] = fmaxf(a, b);
+      cm[c] = fmaxf(fmaxf(a, b), -INFINITY);  // a chunk of NaNs counts as empty
       m = fmaxf(m, cm[c]);
     }
   }
@@ -445,7 +445,7 @@ constexpr int kHeadRowWarps = 4;
 template <bool BWD>
 __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const HeadRowArgs a) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
-  __shared__ int sid[kHeadRowWarps][kHeadMaxIds];
+  __shared__ int sid[kHeadRowWarps][kHeadMaxIds], ordered[kHeadRowWarps][kHeadMaxIds];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kHeadRowWarps + w;
   if (row >= a.M) return;  // whole warps
@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
       const int id = sid[w][i];
       int before = 0;
       for (int j = 0; j < a.n; ++j) before += sid[w][j] < id || (sid[w][j] == id && j < i);
+      ordered[w][before] = id;
       a.sorted[static_cast<size_t>(row) * a.n + before] = make_int2(id, BWD ? __float_as_int(coef[u]) : i);
       if (BWD && a.sorted_logit != nullptr)
         a.sorted_logit[static_cast<size_t>(row) * a.n + before] = a.id_logit[static_cast<size_t>(row) * a.n + i];
@@ -507,20 +508,13 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
     const int tiles = (a.V + kHeadTile - 1) / kHeadTile;
     uint8_t* first = a.first + static_cast<size_t>(row) * tiles;
     for (int t = lane; t < tiles; t += 32) {
-      int before = 0;
-      if (a.n <= 8) {
-        for (int j = 0; j < a.n; ++j) before += sid[w][j] < t * kHeadTile;
-      } else {  // sid is not sorted: count with the sorted copy
-        const int2* so = a.sorted + static_cast<size_t>(row) * a.n;
-        int lo = 0, hi = a.n;
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (so[mid].x < t * kHeadTile) lo = mid + 1;
-          else hi = mid;
-        }
-        before = lo;
+      int lo = 0, hi = a.n;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ordered[w][mid] < t * kHeadTile) lo = mid + 1;
+        else hi = mid;
       }
-      first[t] = static_cast<uint8_t>(before);
+      first[t] = static_cast<uint8_t>(lo);
     }
   }
   if (!BWD && a.bound != nullptr && lane < a.kp) a.bound[static_cast<size_t>(row) * a.kp + lane] = 0u;
@@ -587,29 +581,38 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
   }
 }
 
-// One block a row, with alternatives: as head_finalize_kernel (no loss), then the k best.  The
-// chunks that reach the row's bound go to a list, 2048 chunks a round; their logits, as far as
-// they beat the k-th key known, to a buffer that is cut back to the k largest when it fills up
-// (usually never: about k·log k keys reach the bound).  The buffer's order varies from run to
-// run, the k largest keys do not.
-constexpr int kTopThreads = 256, kTopWarps = kTopThreads / 32, kTopBuf = 1024, kTopRound = 2048;
+// One block a row, with alternatives: as head_finalize_kernel (no loss), then the k best.  First the
+// k best chunks by their maxima (an element of another chunk has k better ones), from those that
+// reach the row's bound; then the k best elements of these.  Bound by latency: 4600 maxima are in
+// flight at once, about k·log k of them reach the bound, at most 1024 elements are looked at.
+constexpr int kTopThreads = 512, kTopWarps = kTopThreads / 32, kTopBuf = 1024, kTopPer = 9;
 __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const HeadRowArgs a) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
   __shared__ unsigned long long buf[kTopBuf], top[kHeadMaxTop];
-  __shared__ int2 list[kTopRound];  // (first column, end) of a chunk
   __shared__ float red[kTopWarps][2], groups[kTopWarps][32];
-  __shared__ int list_n, buf_n;
+  __shared__ int buf_n, above;
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x;
   const float4* part = a.part + static_cast<size_t>(row) * a.np;
-  constexpr int HELD = 4;  // partials a thread keeps in registers
+  const int chunks = a.np * a.cpp;
+  const float* cmax = a.cmax + static_cast<size_t>(row) * chunks;
+  constexpr int HELD = 2;  // partials a thread keeps in registers
   float4 held[HELD];
-  float m = -INFINITY, own = -INFINITY;  // own: the largest of the partials' own bounds (few rows)
 #pragma unroll
   for (int u = 0; u < HELD; ++u) {
     const int i = tid + u * kTopThreads;
     held[u] = i < a.np ? part[i] : make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
   }
+  float cm[kTopPer];
+  auto load_maxima = [&](int q0) {
+#pragma unroll
+    for (int u = 0; u < kTopPer; ++u) {
+      const int q = q0 + u * kTopThreads + tid;
+      cm[u] = q < chunks ? cmax[q] : -INFINITY;
+    }
+  };
+  load_maxima(0);
+  float m = -INFINITY, own = -INFINITY;  // own: the largest of the partials' own bounds (few rows)
 #pragma unroll
   for (int u = 0; u < HELD; ++u) {
     m = fmaxf(m, held[u].x);
@@ -665,6 +668,90 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     red[w][0] = s;
     red[w][1] = t;
   }
+
+  // ---- the best chunks: keys (maximum, chunk) above kth
+  unsigned long long kth = ord_f32(low) > 0 ? (static_cast<unsigned long long>(ord_f32(low)) << 32) - 1 : 0;
+  auto push = [&](unsigned long long key) {  // whole warps; the order in buf varies, the set does not
+    const uint32_t keep = __ballot_sync(0xffffffffu, key > kth);
+    int base = 0;
+    if (lane == 0 && keep) base = atomicAdd(&buf_n, __popc(keep));
+    base = __shfl_sync(0xffffffffu, base, 0);
+    if (key > kth) buf[base + __popc(keep & ((1u << lane) - 1u))] = key;
+  };
+  auto cut = [&]() {  // all threads: the k largest of buf_n keys to top (in order) and the head of buf
+    __syncthreads();
+    const int n = buf_n;
+    if (tid < kHeadMaxTop) top[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kTopThreads) {
+      const unsigned long long key = buf[i];
+      int rank = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) rank += buf[j] > key;
+      if (rank < a.k) top[rank] = key;
+    }
+    __syncthreads();
+    if (top[a.k - 1] > kth) kth = top[a.k - 1];
+    if (tid < a.k) buf[tid] = top[tid];
+    if (tid == 0) buf_n = min(n, a.k);
+    __syncthreads();
+  };
+  for (int q0 = 0; q0 < chunks; q0 += kTopPer * kTopThreads) {
+    if (q0 > 0) load_maxima(q0);
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < kTopPer; ++u) {
+      const int q = q0 + u * kTopThreads + tid;
+      mine += q < chunks && top_key(cm[u], q) > kth;
+    }
+    // usually all that reach the bound fit; else (equal maxima) a buffer's half at a time
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (tid == 0) above = buf_n;
+    __syncthreads();
+    if (lane == 0 && mine) atomicAdd(&above, mine);
+    __syncthreads();
+    const bool fits = above <= kTopBuf;
+#pragma unroll 1
+    for (int u = 0; u < kTopPer; ++u) {
+      const int q = q0 + u * kTopThreads + tid;
+      float c = cm[0];
+#pragma unroll
+      for (int i = 1; i < kTopPer; ++i) c = u == i ? cm[i] : c;
+      push(q < chunks ? top_key(c, q) : 0ull);
+      if (!fits) {
+        __syncthreads();
+        if (buf_n > kTopBuf - kTopThreads) cut();
+      }
+    }
+    __syncthreads();
+  }
+  cut();
+
+  // ---- their elements
+  const unsigned long long mine = lane < a.k ? top[lane] : 0ull;
+  unsigned long long key[kHeadMaxTop / kTopWarps];
+#pragma unroll
+  for (int u = 0; u < kHeadMaxTop / kTopWarps; ++u) {
+    const int i = w + u * kTopWarps;
+    const unsigned long long ck = __shfl_sync(0xffffffffu, mine, i);
+    key[u] = 0;
+    if (ck != 0) {
+      const int q = static_cast<int>(0xffffffffu - static_cast<uint32_t>(ck));
+      int col = q * 32, end = a.V;
+      if (a.few) {
+        const int i0 = q / a.cpp;
+        col = hr_first(a.V, i0, a.np) + (q - i0 * a.cpp) * 32;
+        end = min(a.V, hr_first(a.V, i0 + 1, a.np));
+      }
+      if (col + lane < end) {
+        const float z = a.zlog[static_cast<size_t>(row) * a.V + col + lane];
+        if (z == z) key[u] = top_key(z, col + lane);
+      }
+    }
+  }
+  // the k-th chunk's maximum is the least an element can need
+  const unsigned long long least = top[a.k - 1];
+  kth = least != 0 ? (least >> 32 << 32) - 1 : 0;
   __syncthreads();
   s = t = 0.0f;
 #pragma unroll
@@ -674,6 +761,7 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   }
   const float ls = logf(s);
   if (tid == 0) {
+    buf_n = 0;
     a.lse_out[row] = fmaf(m, kLn2, ls);
     if (a.entropy != nullptr) a.entropy[row] = ls - kLn2 * (t / s);
   }
@@ -684,77 +772,15 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     if (id != a.ignore) lp = id >= 0 && id < a.V ? fmaf(a.id_logit[at], a.c2, -m) * kLn2 - ls : NAN;
     a.logprob[at] = lp;
   }
-
-  // ---- the alternatives: keys above kth may be among the k best
-  unsigned long long kth = ord_f32(low) > 0 ? (static_cast<unsigned long long>(ord_f32(low)) << 32) - 1 : 0;
-  const int chunks = a.np * a.cpp;
-  const float* cmax = a.cmax + static_cast<size_t>(row) * chunks;
-  const float* zrow = a.zlog + static_cast<size_t>(row) * a.V;
-  auto cut = [&]() {  // all threads: the k largest of buf_n keys to top and the head of buf
-    __syncthreads();
-    const int n = buf_n;
-    if (tid < kHeadMaxTop) top[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kTopThreads) {
-      const unsigned long long key = buf[i];
-      int rank = 0;
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) rank += buf[j] > key;
-      if (rank < a.k) top[rank] = key;
-    }
-    __syncthreads();
-    if (top[a.k - 1] > kth) kth = top[a.k - 1];
-    if (tid < a.k) buf[tid] = top[tid];
-    if (tid == 0) buf_n = min(n, a.k);
-    __syncthreads();
-  };
-  for (int q0 = 0; q0 < chunks; q0 += kTopRound) {
-    if (tid == 0) list_n = 0;
-    __syncthreads();
-    float cm[kTopRound / kTopThreads];
+  __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kTopRound / kTopThreads; ++u) {
-      const int q = q0 + u * kTopThreads + tid;
-      cm[u] = q < chunks ? cmax[q] : -INFINITY;
-    }
-#pragma unroll
-    for (int u = 0; u < kTopRound / kTopThreads; ++u) {
-      const int q = q0 + u * kTopThreads + tid;
-      if (q < chunks && cm[u] >= low) {
-        int2 e = make_int2(q * 32, a.V);
-        if (a.few) {
-          const int i = q / a.cpp;
-          e = make_int2(hr_first(a.V, i, a.np) + (q - i * a.cpp) * 32, min(a.V, hr_first(a.V, i + 1, a.np)));
-        }
-        if (top_key(cm[u], e.x) > kth) list[atomicAdd(&list_n, 1)] = e;
-      }
-    }
-    __syncthreads();
-    const int ln = list_n;
-    for (int i0 = 0; i0 < ln;) {
-      const int room = min((kTopBuf - buf_n) / 32, ln - i0);  // chunks that fit: 16 at least
-      __syncthreads();
-      for (int i = i0 + w; i < i0 + room; i += kTopWarps) {
-        const int2 e = list[i];
-        unsigned long long key = 0;
-        if (e.x + lane < e.y) key = top_key(zrow[e.x + lane], e.x + lane);
-        const uint32_t keep = __ballot_sync(0xffffffffu, key > kth);
-        int base = 0;
-        if (lane == 0 && keep) base = atomicAdd(&buf_n, __popc(keep));
-        base = __shfl_sync(0xffffffffu, base, 0);
-        if (key > kth) buf[base + __popc(keep & ((1u << lane) - 1u))] = key;
-      }
-      i0 += room;
-      __syncthreads();
-      if (buf_n > kTopBuf / 2) cut();
-    }
-  }
+  for (int u = 0; u < kHeadMaxTop / kTopWarps; ++u) push(key[u]);
   cut();
   if (tid < a.k) {
-    const unsigned long long key = top[tid];
+    const unsigned long long best = top[tid];
     const size_t at = static_cast<size_t>(row) * a.k + tid;
-    a.top_ids[at] = key != 0 ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
-    a.top_logprob[at] = key != 0 ? fmaf(unord_f32(static_cast<uint32_t>(key >> 32)), a.c2, -m) * kLn2 - ls : NAN;
+    a.top_ids[at] = best != 0 ? static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best)) : -1;
+    a.top_logprob[at] = best != 0 ? fmaf(unord_f32(static_cast<uint32_t>(best >> 32)), a.c2, -m) * kLn2 - ls : NAN;
   }
 }
 

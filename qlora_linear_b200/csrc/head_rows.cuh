@@ -3,15 +3,17 @@
 //
 // Bound by HBM: the head W [V, D] is read once, 2·V·D bytes, against 2·M·V·D flops.  One CTA
 // per SM owns a contiguous range of vocabulary entries (multiples of 16, so the ranges differ
-// by at most 16) and walks it in tiles of up to 256 entries; X stays in L2.  Per tile the
-// tensor core computes the 128 × 256 accumulator of all rows (unused rows hold whatever shared
+// by at most 16) and walks it in tiles of up to 128 entries; X stays in L2.  Per tile the
+// tensor core computes the 128 × 128 accumulator of all rows (unused rows hold whatever shared
 // memory held; nobody reads them): half of what a CTA pair's 256 rows would cost for the same
 // bytes of W.  The statistics and the alternatives' bound stay with the CTA over its whole range,
 // so a row leaves one partial a CTA.
 //
-// W goes through a ring of stages of 64 of the D columns: a full tile in one TMA box of 256
-// entries, a range's last tile in boxes of 16.  The stages' number follows from what X leaves of
-// shared memory (6 up to 16 rows, 4 at 128).
+// W goes through a ring of stages of 128 entries × 128 of the D columns, which HBM serves in
+// 256-byte pieces (V = 128256, D = 4096, 1 row: 182 us with them, 186 us with 256 entries × 64,
+// 196 us with 64 × 256; V = 32000, D = 8192: 121, 140 and 122 us).  A range's last tile takes boxes
+// of 64, 32 and 16 entries.  The stages' number follows from what X leaves of shared memory (6 up
+// to 8 rows, 3 at 128).
 // Roles: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warps 2-5 epilogue (thread =
 // row).  Every wait is bounded.
 #pragma once
@@ -21,8 +23,9 @@
 namespace lora {
 
 constexpr int HR_ROWS = 128;        // rows at most
-constexpr int HR_BN = 256;          // vocabulary entries a tile
-constexpr int HR_BK = 64;           // of D per stage
+constexpr int HR_BN = 128;          // vocabulary entries a tile
+constexpr int HR_BK = 128;          // of D per stage: two 64-wide swizzle atoms
+constexpr int HR_ATOMS = HR_BK / 64;
 constexpr int HR_UNIT = 16;         // granularity of the CTAs' ranges
 constexpr int HR_MAX_STAGES = 6;
 constexpr int HR_THREADS = 192;
@@ -38,7 +41,7 @@ __host__ __device__ constexpr int hr_x_bytes(int M) { return (M + 7) / 8 * 8 * H
 // Stages that fit; the MMA reads 128 rows of X from any stage, so as many must fit behind the
 // last stage's W.
 __host__ __device__ constexpr int hr_stages(int M) {
-  const int behind = 128 * HR_BK * 2 - hr_x_bytes(M);
+  const int behind = (128 - (M + 7) / 8 * 8) * 128;
   const int n = (HR_SMEM_MAX - 1024 - behind) / (HR_W_BYTES + hr_x_bytes(M));
   return n < HR_MAX_STAGES ? n : HR_MAX_STAGES;
 }
@@ -55,6 +58,11 @@ struct HeadRowsParams {
   int stages;
   uint32_t* status;
   uint64_t wait_ns;
+};
+
+// The head in boxes of 64 columns × 128, 64, 32 and 16 entries.
+struct HeadRowsMaps {
+  CUtensorMap box[4];
 };
 
 // A third look at the tile, for the alternatives: the column groups' maxima over the CTA's range
@@ -87,8 +95,8 @@ __device__ __forceinline__ float head_rows_bound(const HeadArgs& h, uint32_t tba
 }
 
 __global__ void __launch_bounds__(HR_THREADS, 1)
-    head_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmW16, const HeadRowsParams p) {
+    head_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ HeadRowsMaps tmW,
+                     const HeadRowsParams p) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
   extern __shared__ __align__(1024) uint8_t hr_raw[];
   __shared__ __align__(8) uint64_t full[HR_MAX_STAGES], empty[HR_MAX_STAGES], tfull[2], tempty[2], drain;
@@ -119,8 +127,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
     never_s = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmX);
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmW16);
+    tma_prefetch_desc(&tmW.box[0]);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_slot), 512);
@@ -151,12 +158,18 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
           const uint32_t sW = smem_u32(smem + stage * stage_bytes);
           const uint32_t bar = smem_u32(&full[stage]);
           mbar_arrive_expect_tx(bar, rows * HR_BK * 2 + xbytes);
-          if (rows == HR_BN) {
-            tma_load_2d(sW, &tmW, bar, kb * HR_BK, v0);
-          } else {
-            for (int u = 0; u < rows; u += HR_UNIT) tma_load_2d(sW + u * HR_BK * 2, &tmW16, bar, kb * HR_BK, v0 + u);
+#pragma unroll
+          for (int a = 0; a < HR_ATOMS; ++a) {
+            const int x = kb * HR_BK + a * 64;
+            int u = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (rows & (HR_BN >> i)) {
+                tma_load_2d(sW + a * (HR_W_BYTES / HR_ATOMS) + u * 128, &tmW.box[i], bar, x, v0 + u);
+                u += HR_BN >> i;
+              }
+            tma_load_2d(sW + HR_W_BYTES + a * (xbytes / HR_ATOMS), &tmX, bar, x, 0);
           }
-          tma_load_2d(sW + HR_W_BYTES, &tmX, bar, kb * HR_BK, 0);
           ++fills;
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
@@ -185,8 +198,10 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
           const uint32_t sW = smem_u32(smem + stage * stage_bytes);
 #pragma unroll
           for (int k = 0; k < HR_BK / 16; ++k)
-            tc_mma_bf16(tmem_base + acc * HR_BN, sdesc_sw128(sW + HR_W_BYTES + k * 32, 16, 1024),
-                        sdesc_sw128(sW + k * 32, 16, 1024), idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            tc_mma_bf16(tmem_base + acc * HR_BN,
+                        sdesc_sw128(sW + HR_W_BYTES + (k >> 2) * (xbytes / HR_ATOMS) + (k & 3) * 32, 16, 1024),
+                        sdesc_sw128(sW + (k >> 2) * (HR_W_BYTES / HR_ATOMS) + (k & 3) * 32, 16, 1024), idesc,
+                        (kb > 0 || k > 0) ? 1u : 0u);
           tc_commit(smem_u32(&empty[stage]));
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }

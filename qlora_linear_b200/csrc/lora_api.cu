@@ -1378,11 +1378,11 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     p.stages = hr_stages(p.M);
     p.status = status;
     p.wait_ns = wait_limit_ns();
-    CUtensorMap tx, tw, tw16;
-    TRY(tmap_bf16(&tx, X, D, M, HR_BK, static_cast<uint32_t>((M + 7) / 8 * 8)));
-    TRY(tmap_bf16(&tw, W->data, D, V, HR_BK, HR_BN));
-    TRY(tmap_bf16(&tw16, W->data, D, V, HR_BK, HR_UNIT));
-    launch_k(head_rows_kernel, dim3(l.np), dim3(HR_THREADS), HR_SMEM_MAX, st, tx, tw, tw16, p);
+    CUtensorMap tx;
+    HeadRowsMaps tw;
+    TRY(tmap_bf16(&tx, X, D, M, 64, static_cast<uint32_t>((M + 7) / 8 * 8)));
+    for (int i = 0; i < 4; ++i) TRY(tmap_bf16(&tw.box[i], W->data, D, V, 64, HR_BN >> i));
+    launch_k(head_rows_kernel, dim3(l.np), dim3(HR_THREADS), HR_SMEM_MAX, st, tx, tw, p);
     count_launch();
     TRY(last_launch());
     r.M = p.M;
