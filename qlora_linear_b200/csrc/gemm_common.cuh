@@ -17,7 +17,7 @@ struct HeadArgs {
   unsigned* bound;           // forward: [M][kp] group maxima over the tiles seen so far
   float* cmax;               // forward: [M][tiles · chunks] maxima of every 32 columns
   float* zlog;               // forward: [M][V] accumulators of the chunks that may matter
-  float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, few rows: own bound)
+  float4* part;              // forward: [M][tiles] (max, Σe, Σd·e, -)
   const uint8_t* first;      // [M][tiles of the vocabulary] tokens before each tile
   __nv_bfloat16* expz;       // [M][V] 2^{y - tau}, or null
   float* tau;                // [M][tiles], with expz

@@ -18,8 +18,8 @@
 // tiles are joined by Σe ← 2^{m-M}·Σe, Σd·e ← 2^{m-M}·(Σd·e + (m - M)·Σe).  Given tokens and
 // alternatives are kept as accumulators.
 //
-// The alternatives.  Every 32 columns (a chunk) leave their maximum, and their 32 logits only
-// if that reaches a lower bound of the row's k-th largest logit; head_finalize_top_kernel then
+// The alternatives.  Every 32 columns (a chunk) leave their maximum, and (pair kernel) their 32
+// logits only if that reaches a lower bound of the row's k-th largest logit; head_finalize_top_kernel then
 // looks at the few chunks that reach the final bound.  The bound: cut what was seen so far into
 // kp >= k disjoint groups; the least of the groups' maxima is at most the k-th largest.  It
 // never falls, so a chunk that reaches a later bound has been written.  In random order about
@@ -101,34 +101,6 @@ __device__ __forceinline__ float head_tile_max(uint32_t tbase, int nv, float (&c
     }
   }
   return m;
-}
-
-// Second pass: the sums about m = c2·(the maximum) and, of the chunks in `hits`, the logits to
-// zrow.
-__device__ __forceinline__ RowStats head_tile_sums(uint32_t tbase, int nv, float c2, float m, uint32_t hits,
-                                                   float* zrow) {
-  float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
-#pragma unroll 1
-  for (int c = 0; c * 32 < nv; ++c) {
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(tbase + c * 32, v);
-    tmem_ld_wait();
-    const int n = nv - c * 32;
-    if ((hits >> c) & 1u) head_store_chunk(v, n, zrow + c * 32);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q * 8 < n) {  // n is a multiple of 8
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = fmaf(__uint_as_float(v[8 * q + j]), c2, -m);
-          const float e = ex2_approx(d);
-          s[j & 1] += e;
-          t[j & 1] = fmaf(d, e, t[j & 1]);
-        }
-      }
-    __syncwarp();
-  }
-  return RowStats{m, s[0] + s[1], t[0] + t[1]};
 }
 
 // A row's first given token at or above a tile: its index among the sorted ones, its entry
@@ -407,8 +379,8 @@ struct HeadRowArgs {
   const float* id_logit;   // [M][n]
   int k, kp;
   int cpp;                 // chunks a partial
-  int few;                 // partials are head_rows_kernel's (col0 of hr_first), else 128 columns each
-  const float* cmax;       // [M][np·cpp] chunk maxima (-inf past a partial's last)
+  int ctas;                // chunks are head_rows_kernel's, cpp a CTA; 0: cpp a partial of 128 columns
+  const float* cmax;       // [M][chunks] maxima (-inf past a CTA's or the vocabulary's last)
   const float* zlog;       // [M][V] logits of the chunks that were kept
   float* logprob;          // [M][n] or null
   float* entropy;          // [M] or null
@@ -520,9 +492,9 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
   if (!BWD && a.bound != nullptr && lane < a.kp) a.bound[static_cast<size_t>(row) * a.kp + lane] = 0u;
 }
 
-// First vocabulary entry of partial i of np of head_rows_kernel: ranges of multiples of 16.
-__host__ __device__ __forceinline__ int hr_first(int V, int i, int np) {
-  return static_cast<int>(static_cast<long long>((V + 15) / 16) * i / np) * 16;
+// First vocabulary entry of CTA i of head_rows_kernel: ranges of multiples of 16.
+__host__ __device__ __forceinline__ int hr_first(int V, int i, int ctas) {
+  return static_cast<int>(static_cast<long long>((V + 15) / 16) * i / ctas) * 16;
 }
 
 // One warp a row: joins the row's partials (in a fixed order), and from them the
@@ -539,6 +511,7 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
   float s = 0.0f, t = 0.0f;
   for (int i = lane; i < a.np; i += 32) {
     const float4 q = part[i];
+    if (q.y == 0.0f) continue;  // no entries
     const float d = q.x * a.c2 - m, e = exp2f(d);
     s = fmaf(q.y, e, s);
     t = fmaf(fmaf(d, q.y, q.z), e, t);
@@ -594,14 +567,14 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int row = blockIdx.x;
   const float4* part = a.part + static_cast<size_t>(row) * a.np;
-  const int chunks = a.np * a.cpp;
+  const int chunks = (a.ctas > 0 ? a.ctas : a.np) * a.cpp;
   const float* cmax = a.cmax + static_cast<size_t>(row) * chunks;
   constexpr int HELD = 2;  // partials a thread keeps in registers
   float4 held[HELD];
 #pragma unroll
   for (int u = 0; u < HELD; ++u) {
     const int i = tid + u * kTopThreads;
-    held[u] = i < a.np ? part[i] : make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
+    held[u] = i < a.np ? part[i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
   }
   float cm[kTopPer];
   auto load_maxima = [&](int q0) {
@@ -612,47 +585,36 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     }
   };
   load_maxima(0);
-  float m = -INFINITY, own = -INFINITY;  // own: the largest of the partials' own bounds (few rows)
+  float m = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < HELD; ++u) {
-    m = fmaxf(m, held[u].x);
-    own = fmaxf(own, held[u].w);
-  }
-  for (int i = tid + HELD * kTopThreads; i < a.np; i += kTopThreads) {
-    const float4 q = part[i];
-    m = fmaxf(m, q.x);
-    own = fmaxf(own, q.w);
-  }
+  for (int u = 0; u < HELD; ++u) m = fmaxf(m, held[u].x);
+  for (int i = tid + HELD * kTopThreads; i < a.np; i += kTopThreads) m = fmaxf(m, part[i].x);
   // few rows: the partials' maxima in groups (i mod kp: the lane mod kp); the least group's is a
   // bound
   float g = m;
   for (int o = a.kp; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
   groups[w][lane] = g;
   m = warp_max(m);
-  own = warp_max(own);
-  if (lane == 0) {
-    red[w][0] = m;
-    red[w][1] = own;
-  }
+  if (lane == 0) red[w][0] = m;
   if (tid == 0) buf_n = 0;
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < kTopWarps; ++u) {
     m = fmaxf(m, red[u][0]);
-    own = fmaxf(own, red[u][1]);
     g = fmaxf(g, groups[u][lane]);
   }
   m *= a.c2;
   float low;
-  if (a.few) {
+  if (a.ctas > 0) {
     for (int o = 1; o < a.kp; o <<= 1) g = fminf(g, __shfl_xor_sync(0xffffffffu, g, o));
-    low = fmaxf(g, own);
+    low = g;
   } else {
     const uint32_t o = lane < a.kp ? a.bound[static_cast<size_t>(row) * a.kp + lane] : 0xffffffffu;
     low = unord_f32(max(__reduce_min_sync(0xffffffffu, o), ord_f32(-INFINITY)));  // 0: an empty group
   }
   float s = 0.0f, t = 0.0f;
   auto join = [&](const float4& q) {
+    if (q.y == 0.0f) return;  // no entries
     const float d = q.x * a.c2 - m, e = exp2f(d);
     s = fmaf(q.y, e, s);
     t = fmaf(fmaf(d, q.y, q.z), e, t);
@@ -738,10 +700,10 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     if (ck != 0) {
       const int q = static_cast<int>(0xffffffffu - static_cast<uint32_t>(ck));
       int col = q * 32, end = a.V;
-      if (a.few) {
+      if (a.ctas > 0) {
         const int i0 = q / a.cpp;
-        col = hr_first(a.V, i0, a.np) + (q - i0 * a.cpp) * 32;
-        end = min(a.V, hr_first(a.V, i0 + 1, a.np));
+        col = hr_first(a.V, i0, a.ctas) + (q - i0 * a.cpp) * 32;
+        end = min(a.V, hr_first(a.V, i0 + 1, a.ctas));
       }
       if (col + lane < end) {
         const float z = a.zlog[static_cast<size_t>(row) * a.V + col + lane];

@@ -3,19 +3,23 @@
 //
 // Bound by HBM: the head W [V, D] is read once, 2·V·D bytes, against 2·M·V·D flops.  One CTA
 // per SM owns a contiguous range of vocabulary entries (multiples of 16, so the ranges differ
-// by at most 16) and walks it in tiles of up to 128 entries; X stays in L2.  Per tile the
-// tensor core computes the 128 × 128 accumulator of all rows (unused rows hold whatever shared
-// memory held; nobody reads them): half of what a CTA pair's 256 rows would cost for the same
-// bytes of W.  The statistics and the alternatives' bound stay with the CTA over its whole range,
-// so a row leaves one partial a CTA.
+// by at most 16) and walks it in tiles of up to 128; X stays in L2.  The vocabulary is the
+// MMA's M dimension (128) and the rows its N (16 to 128): the tensor core works for the rows
+// there are.  (With the roles the other way round, 128 rows of which few are real, the GPU's power
+// limit lowered the clock and one row took 194 us instead of 171.)
 //
 // W goes through a ring of stages of 128 entries × 128 of the D columns, which HBM serves in
-// 256-byte pieces (V = 128256, D = 4096, 1 row: 182 us with them, 186 us with 256 entries × 64,
-// 196 us with 64 × 256; V = 32000, D = 8192: 121, 140 and 122 us).  A range's last tile takes boxes
-// of 64, 32 and 16 entries.  The stages' number follows from what X leaves of shared memory (6 up
-// to 8 rows, 3 at 128).
-// Roles: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warps 2-5 epilogue (thread =
-// row).  Every wait is bounded.
+// 256-byte pieces, each CTA starting at another column (V = 128256, D = 4096, 1 row: 182 us;
+// 186 us with 256 entries × 64, 196 us with 64 × 256).  A range's last tile takes boxes of 64, 32
+// and 16 entries.
+//
+// Epilogue: a lane holds one entry's logits of 32 rows.  Sums over the 32 entries of a warp go
+// by transposing reductions (31 shuffles for 32 rows, lane i ending with row i), so a warp keeps the
+// running statistics of row i in lane i, and leaves one partial a CTA, warp and row.  A warp's 32
+// entries are a chunk: with alternatives every chunk's maximum and all logits are written (4·M·V
+// bytes, coalesced).
+// Roles: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warps 2-5 epilogue.  Every wait
+// is bounded.
 #pragma once
 
 #include "head.cuh"
@@ -29,6 +33,7 @@ constexpr int HR_ATOMS = HR_BK / 64;
 constexpr int HR_UNIT = 16;         // granularity of the CTAs' ranges
 constexpr int HR_MAX_STAGES = 6;
 constexpr int HR_THREADS = 192;
+constexpr int HR_WARPS = 4;         // epilogue warps: partials a CTA
 constexpr int HR_W_BYTES = HR_BN * HR_BK * 2;  // 32 KB
 constexpr int HR_SMEM_MAX = 232448 - 2048;  // dynamic; the barriers are static
 
@@ -36,13 +41,11 @@ constexpr int HR_SMEM_MAX = 232448 - 2048;  // dynamic; the barriers are static
 __host__ __device__ constexpr int hr_ctas(long long V) {
   return static_cast<int>((V + 31) / 32 < 148 ? (V + 31) / 32 : 148);
 }
-// Bytes of X in a stage: the rows rounded up to the 8-row swizzle atom.
-__host__ __device__ constexpr int hr_x_bytes(int M) { return (M + 7) / 8 * 8 * HR_BK * 2; }
-// Stages that fit; the MMA reads 128 rows of X from any stage, so as many must fit behind the
-// last stage's W.
+// Rows of the MMA's N dimension, and X's bytes in a stage.
+__host__ __device__ constexpr int hr_n(int M) { return (M + 15) / 16 * 16; }
+__host__ __device__ constexpr int hr_x_bytes(int M) { return hr_n(M) * HR_BK * 2; }
 __host__ __device__ constexpr int hr_stages(int M) {
-  const int behind = (128 - (M + 7) / 8 * 8) * 128;
-  const int n = (HR_SMEM_MAX - 1024 - behind) / (HR_W_BYTES + hr_x_bytes(M));
+  const int n = (HR_SMEM_MAX - 1024) / (HR_W_BYTES + hr_x_bytes(M));
   return n < HR_MAX_STAGES ? n : HR_MAX_STAGES;
 }
 // Chunks of 32 entries of the longest range.
@@ -51,7 +54,7 @@ __host__ __device__ constexpr int hr_chunks(long long V) {
 }
 
 struct HeadRowsParams {
-  HeadArgs h;              // sorted and bound are not used; part is [M][CTAs]
+  HeadArgs h;              // sorted and bound are not used; part is [M][4·CTAs]
   int cpp;                 // chunks a CTA (cmax is [M][CTAs · cpp])
   const int32_t* ids;      // [M][n]
   int M, V, D;
@@ -65,33 +68,19 @@ struct HeadRowsMaps {
   CUtensorMap box[4];
 };
 
-// A third look at the tile, for the alternatives: the column groups' maxima over the CTA's range
-// so far, and the least of the kp groups that they fold into.
-__device__ __forceinline__ float head_rows_bound(const HeadArgs& h, uint32_t tbase, int nv, float (&groups)[32]) {
-#pragma unroll 1
-  for (int c = 0; c * 32 < nv; ++c) {
-    uint32_t v[32];
-    tmem_ld_32x32b_x32(tbase + c * 32, v);
-    tmem_ld_wait();
-    const int n = nv - c * 32;
+// x[i] of every lane reduced over the lanes, into lane i.
+template <typename Op>
+__device__ __forceinline__ float transpose_reduce(float (&x)[32], int lane, Op op) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < n) groups[j] = fmaxf(groups[j], __uint_as_float(v[j]));
-  }
-  float g[32];
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool hi = lane & s;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) g[j] = groups[j];
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1)
-    if (h.kp <= s) {
-#pragma unroll
-      for (int j = 0; j < s; ++j) g[j] = fmaxf(g[j], g[j + s]);
+    for (int j = 0; j < s; ++j) {
+      const float give = hi ? x[j] : x[j + s], keep = hi ? x[j + s] : x[j];
+      x[j] = op(keep, __shfl_xor_sync(0xffffffffu, give, s));
     }
-  float low = g[0];
-#pragma unroll
-  for (int j = 1; j < 32; ++j)
-    if (j < h.kp) low = fminf(low, g[j]);
-  return low;
+  }
+  return x[0];
 }
 
 __global__ void __launch_bounds__(HR_THREADS, 1)
@@ -120,7 +109,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull[a]), 1);
-      mbar_init(smem_u32(&tempty[a]), 4);
+      mbar_init(smem_u32(&tempty[a]), HR_WARPS);
     }
     mbar_init(smem_u32(&drain), 1);
     abort_s = 0;
@@ -130,7 +119,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
     tma_prefetch_desc(&tmW.box[0]);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_alloc(smem_u32(&tmem_slot), 2 * HR_ROWS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -145,6 +134,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
       uint32_t phase = 0;
       long long fills = 0;
       bool ok = true;
+      const int shift = static_cast<int>(static_cast<long long>(blockIdx.x) * nkb / gridDim.x);
       for (int t = 0; ok && t < ntiles; ++t) {
         const int v0 = r0 + t * HR_BN;
         const int rows = min(HR_BN, r1 - v0);  // a multiple of 16
@@ -155,12 +145,13 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
         }
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
+          const int kx = kb + shift < nkb ? kb + shift : kb + shift - nkb;
           const uint32_t sW = smem_u32(smem + stage * stage_bytes);
           const uint32_t bar = smem_u32(&full[stage]);
           mbar_arrive_expect_tx(bar, rows * HR_BK * 2 + xbytes);
 #pragma unroll
           for (int a = 0; a < HR_ATOMS; ++a) {
-            const int x = kb * HR_BK + a * 64;
+            const int x = kx * HR_BK + a * 64;
             int u = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -184,12 +175,13 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
+      // entries a last tile did not load hold what shared memory held: their lanes are not used
+      const uint32_t idesc = idesc_bf16_f32(HR_BN, hr_n(p.M), false, false);
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       int acc = 0;
       bool ok = true;
       for (int t = 0; ok && t < ntiles; ++t) {
-        const uint32_t idesc = idesc_bf16_f32(HR_ROWS, min(HR_BN, r1 - r0 - t * HR_BN), false, false);
         if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, wc)) break;
         tc_fence_after();
         for (int kb = 0; kb < nkb; ++kb) {
@@ -198,9 +190,9 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
           const uint32_t sW = smem_u32(smem + stage * stage_bytes);
 #pragma unroll
           for (int k = 0; k < HR_BK / 16; ++k)
-            tc_mma_bf16(tmem_base + acc * HR_BN,
-                        sdesc_sw128(sW + HR_W_BYTES + (k >> 2) * (xbytes / HR_ATOMS) + (k & 3) * 32, 16, 1024),
-                        sdesc_sw128(sW + (k >> 2) * (HR_W_BYTES / HR_ATOMS) + (k & 3) * 32, 16, 1024), idesc,
+            tc_mma_bf16(tmem_base + acc * HR_ROWS,
+                        sdesc_sw128(sW + (k >> 2) * (HR_W_BYTES / HR_ATOMS) + (k & 3) * 32, 16, 1024),
+                        sdesc_sw128(sW + HR_W_BYTES + (k >> 2) * (xbytes / HR_ATOMS) + (k & 3) * 32, 16, 1024), idesc,
                         (kb > 0 || k > 0) ? 1u : 0u);
           tc_commit(smem_u32(&empty[stage]));
           if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -215,70 +207,92 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
       mbar_wait(smem_u32(&drain), 0, drain_wc);
     }
   } else {
-    // ------------------------------------------------------------ epilogue (thread = row)
+    // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const bool in = row < p.M;
     const HeadArgs& h = p.h;
-    RowStats st{-INFINITY, 0.0f, 0.0f};
-    float raw = -INFINITY;  // the largest accumulator (st.m in units of log 2)
-    float groups[32];  // maxima of the CTA's logits by tile column mod kp: their least is a bound
+    const int np = static_cast<int>(gridDim.x) * HR_WARPS, pi = static_cast<int>(blockIdx.x) * HR_WARPS + quarter;
+    constexpr int GROUPS = HR_ROWS / 32;
+    RowStats st[GROUPS];  // of row 32·g + lane
+    float raw[GROUPS];    // their largest accumulators (st.m in units of log 2)
 #pragma unroll
-    for (int j = 0; j < 32; ++j) groups[j] = -INFINITY;
-    float low = -INFINITY;
-    const size_t at = static_cast<size_t>(row) * gridDim.x + blockIdx.x;
+    for (int g = 0; g < GROUPS; ++g) {
+      st[g] = RowStats{-INFINITY, 0.0f, 0.0f};
+      raw[g] = -INFINITY;
+    }
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int t = 0; t < ntiles; ++t) {
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, wc)) { ok = false; break; }
       tc_fence_after();
-      if (quarter * 32 < p.M) {  // a warp without rows has nothing to read
-        const int v0 = r0 + t * HR_BN;
-        const int nv = min(HR_BN, min(r1, p.V) - v0);
-        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * HR_BN;
-        for (int i = 0; i < h.n; ++i) {
-          int col = -1;
-          if (in) {
-            const uint32_t off = static_cast<uint32_t>(p.ids[static_cast<size_t>(row) * h.n + i]) - static_cast<uint32_t>(v0);
-            if (off < static_cast<uint32_t>(nv)) col = static_cast<int>(off);
-          }
-          uint32_t want = __ballot_sync(0xffffffffu, col >= 0);
-          while (want) {
-            const int at = __shfl_sync(0xffffffffu, col, __ffs(want) - 1);
-            const float z = __uint_as_float(tmem_ld_32x32b_x1(tbase + at));
-            if (col == at) h.id_logit[static_cast<size_t>(row) * h.n + i] = z;
-            want &= ~__ballot_sync(0xffffffffu, col == at);
-          }
-        }
-        float cm[HR_BN / 32];
-        const float tile_max = head_tile_max<HR_BN / 32>(tbase, nv, cm), m = tile_max * h.c2;
-        raw = fmaxf(raw, tile_max);
-        uint32_t hits = 0;
-        if (h.k > 0) {
-          low = head_rows_bound(h, tbase, nv, groups);
-          if (in) {
+      const int c0 = r0 + t * HR_BN + quarter * 32;  // the warp's chunk of entries
+      const int nc = min(32, min(r1, p.V) - c0);     // <= 0: past the range
+      const bool valid = lane < nc;
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * HR_ROWS;
 #pragma unroll
-            for (int c = 0; c < HR_BN / 32; ++c)
-              if (t * (HR_BN / 32) + c < p.cpp) {
-                h.cmax[at * p.cpp + t * (HR_BN / 32) + c] = cm[c];
-                if (c * 32 < nv && cm[c] >= low) hits |= 1u << c;
-              }
+      for (int g = 0; g < GROUPS; ++g) {
+        if (g * 32 >= p.M || nc <= 0) break;  // warp-uniform
+        const int row = g * 32 + lane;
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tbase + g * 32, v);  // columns past the MMA's N are not used
+        tmem_ld_wait();
+        // given tokens: row i's ids are looked at by lane i, their logits stored by the lanes that
+        // hold their entries
+        for (int i = 0; i < h.n; ++i) {
+          uint32_t off = 0xffffffffu;
+          if (row < p.M)
+            off = static_cast<uint32_t>(p.ids[static_cast<size_t>(row) * h.n + i]) - static_cast<uint32_t>(c0);
+          uint32_t want = __ballot_sync(0xffffffffu, off < static_cast<uint32_t>(nc));
+          while (want) {
+            const int r = __ffs(want) - 1;
+            want &= want - 1;
+            const uint32_t at = __shfl_sync(0xffffffffu, off, r);
+            const uint32_t z = tmem_ld_32x32b_x1(tbase + g * 32 + r);
+            if (lane == at) h.id_logit[static_cast<size_t>(g * 32 + r) * h.n + i] = __uint_as_float(z);
+            __syncwarp();
           }
-          __syncwarp();
         }
-        st = join_stats(st, head_tile_sums(tbase, nv, h.c2, m, hits,
-                                           h.zlog + static_cast<size_t>(row) * p.V + v0));
+        if (h.k > 0 && valid) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (g * 32 + j < p.M) h.zlog[static_cast<size_t>(g * 32 + j) * p.V + c0 + lane] = __uint_as_float(v[j]);
+        }
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = valid ? __uint_as_float(v[j]) : -INFINITY;
+        const float top = transpose_reduce(x, lane, [](float a, float b) { return fmaxf(a, b); });
+        if (h.k > 0 && row < p.M)
+          h.cmax[(static_cast<size_t>(row) * gridDim.x + blockIdx.x) * p.cpp + t * (HR_BN / 32) + quarter] =
+              fmaxf(top, -INFINITY);
+        const float m = top * h.c2;
+        float y[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float d = fmaf(__uint_as_float(v[j]), h.c2, -__shfl_sync(0xffffffffu, m, j));
+          const float e = ex2_approx(d);
+          x[j] = valid ? e : 0.0f;
+          y[j] = valid ? d * e : 0.0f;
+        }
+        const float s = transpose_reduce(x, lane, [](float a, float b) { return a + b; });
+        const float dt = transpose_reduce(y, lane, [](float a, float b) { return a + b; });
+        st[g] = join_stats(st[g], RowStats{m, s, dt});
+        raw[g] = fmaxf(raw[g], top);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tempty[acc]));
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
-    if (ok && in) {
-      h.part[at] = make_float4(raw, st.s, st.t, low);
-      if (h.k > 0)  // a range may be a chunk shorter than the longest
-        for (int c = ntiles * (HR_BN / 32); c < p.cpp; ++c) h.cmax[at * p.cpp + c] = -INFINITY;
+    if (ok) {
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        const int row = g * 32 + lane;
+        if (row >= p.M) continue;
+        h.part[static_cast<size_t>(row) * np + pi] = make_float4(raw[g], st[g].s, st[g].t, 0.0f);
+        // chunks that a shorter range does not have
+        for (int c = (r1 - r0 + 31) / 32 + quarter; h.k > 0 && c < p.cpp; c += HR_WARPS)
+          h.cmax[(static_cast<size_t>(row) * gridDim.x + blockIdx.x) * p.cpp + c] = -INFINITY;
+      }
     }
   }
 
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    tmem_dealloc(tmem_base, 2 * HR_ROWS);
   }
 }
 

@@ -1211,16 +1211,18 @@ inline int pow2_at_least(int k) {
 struct HeadFwdLayout {
   bool few = false;
   long long chunk = 0;  // rows
-  int np = 0, cpp = 0;  // partials a row, chunks a partial
+  int np = 0;           // partials a row
+  int ctas = 0, cpp = 0;  // few rows: CTAs; chunks a CTA or partial
   size_t sorted_off = 0, logit_off = 0, first_off = 0, bound_off = 0, part_off = 0, cmax_off = 0, zlog_off = 0, total = 0;
 };
 HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save) {
   HeadFwdLayout l;
   const int kp = k > 0 ? pow2_at_least(k) : 0;
   l.few = M <= kHeadFewRows && !save;
-  l.np = l.few ? hr_ctas(V) : cdiv(V, kHeadTile);
+  l.ctas = l.few ? hr_ctas(V) : 0;
+  l.np = l.few ? l.ctas * HR_WARPS : cdiv(V, kHeadTile);
   l.cpp = l.few ? hr_chunks(V) : kHeadTile / 32;
-  const size_t maxima = k > 0 ? static_cast<size_t>(l.np) * l.cpp * 4 : 0, logits = k > 0 ? static_cast<size_t>(V) * 4 : 0;
+  const size_t maxima = k > 0 ? static_cast<size_t>(l.few ? l.ctas : l.np) * l.cpp * 4 : 0, logits = k > 0 ? static_cast<size_t>(V) * 4 : 0;
   const size_t first = n > 0 && !l.few ? cdiv(V, kHeadTile) : 0;
   const size_t per_row = 12 * static_cast<size_t>(n) + first + 4 * kp + 16 * static_cast<size_t>(l.np) + maxima + logits;
   long long c = static_cast<long long>(kHeadChunkBytes / per_row) / 256 * 256;
@@ -1359,7 +1361,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
   r.part = h.part;
   r.id_logit = h.id_logit;
   r.cpp = l.cpp;
-  r.few = l.few;
+  r.ctas = l.ctas;
   r.cmax = h.cmax;
   r.zlog = h.zlog;
   r.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
@@ -1380,9 +1382,9 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     p.wait_ns = wait_limit_ns();
     CUtensorMap tx;
     HeadRowsMaps tw;
-    TRY(tmap_bf16(&tx, X, D, M, 64, static_cast<uint32_t>((M + 7) / 8 * 8)));
+    TRY(tmap_bf16(&tx, X, D, M, 64, static_cast<uint32_t>(hr_n(p.M))));
     for (int i = 0; i < 4; ++i) TRY(tmap_bf16(&tw.box[i], W->data, D, V, 64, HR_BN >> i));
-    launch_k(head_rows_kernel, dim3(l.np), dim3(HR_THREADS), HR_SMEM_MAX, st, tx, tw, p);
+    launch_k(head_rows_kernel, dim3(l.ctas), dim3(HR_THREADS), HR_SMEM_MAX, st, tx, tw, p);
     count_launch();
     TRY(last_launch());
     r.M = p.M;
