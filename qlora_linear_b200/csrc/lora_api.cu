@@ -1829,7 +1829,8 @@ size_t lora_head_bwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n,
 
 size_t lora_head_saved_bytes(int64_t M, int64_t V, int32_t n) {
   if (!head_sizes_ok(M, 8, V, n, 0)) return 0;
-  return head_saved_logit_off(M, V) + align256(static_cast<size_t>(M) * n * 4);
+  const size_t b = head_saved_logit_off(M, V) + align256(static_cast<size_t>(M) * n * 4);
+  return b > 0 ? b : 256;  // 0 stands for invalid sizes
 }
 
 lora_status_t lora_logprob_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,

@@ -3,12 +3,13 @@ given tokens with entropy and top alternatives, and distillation from a teacher'
 each with its gradient in the hidden states."""
 from __future__ import annotations
 
-import contextlib
 import dataclasses
 
 import torch
 
 from . import binding as _b
+
+_current_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() takes 7 us
 
 
 @dataclasses.dataclass
@@ -52,14 +53,14 @@ class _HeadLayer:
         self.W, self.ignore_index, self.slice = W, int(ignore_index), int(slice_)
         self.scale = 1.0 / float(temperature)
         self._ws = {}
+        self._sizes = {}
 
-    @contextlib.contextmanager
-    def _on(self, X, stream, *inputs):
-        """Runs the body with X's device and ``stream`` current; yields the stream's handle."""
-        if stream is None and X.device.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream().cuda_stream
-            return
-        with torch.cuda.device(X.device):
+    def _run(self, call, X, stream, *inputs):
+        """``call(handle)`` with X's device and ``stream`` current; returns what it returns."""
+        index = X.device.index
+        if stream is None and index == torch.cuda.current_device():
+            return call(_current_raw_stream(index))  # the usual case, without the context managers
+        with torch.cuda.device(index):
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=X.device)
             elif stream is None:
@@ -69,11 +70,20 @@ class _HeadLayer:
                     if t is not None:
                         t.record_stream(stream)
             with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+                return call(stream.cuda_stream)
+
+    def _bytes(self, fn, *sizes) -> int:
+        """A workspace size, asked for once (it is a function of the sizes alone)."""
+        n = self._sizes.get((fn, sizes))
+        if n is None:
+            if len(self._sizes) >= 4096:
+                self._sizes.clear()
+            n = self._sizes[(fn, sizes)] = fn(*sizes)
+            if n == 0:
+                raise _b.LoraError(_b.LORA_ERR_UNSUPPORTED, fn.__name__)
+        return n
 
     def _workspace(self, nbytes: int, device, stream: int) -> torch.Tensor:
-        if nbytes == 0:
-            raise _b.LoraError(_b.LORA_ERR_UNSUPPORTED, "head workspace")
         if torch.cuda.is_current_stream_capturing():
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
             ws[:256].zero_()
@@ -108,8 +118,8 @@ class _HeadLayer:
 
     @staticmethod
     def _like(t, name, dtype, shape, device):
-        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape)
-                and t.device == device and t.is_contiguous()):
+        if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device
+                and t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
         return t
 
@@ -130,11 +140,11 @@ class _HeadLayer:
         return max(256, min(self.W.N, (1 << 30) // (2 * max(M, 1)) // 256 * 256))
 
     def _saved(self, M, n, device):
-        return torch.empty(_b.head_saved_bytes(M, self.W.N, n), dtype=torch.uint8, device=device)
+        return torch.empty(self._bytes(_b.head_saved_bytes, M, self.W.N, n), dtype=torch.uint8, device=device)
 
     def _bwd_workspace(self, M, n, saved, device, handle):
-        nb = _b.head_bwd_workspace_bytes(M, self.W.K, self.W.N, n, 0 if saved is not None else self._slice(M))
-        return self._workspace(nb, device, handle)
+        slice_ = 0 if saved is not None else self._slice(M)
+        return self._workspace(self._bytes(_b.head_bwd_workspace_bytes, M, self.W.K, self.W.N, n, slice_), device, handle)
 
     def _dX(self, dX, X):
         if dX is None:
@@ -162,7 +172,8 @@ class LoraTokenLogProbs(_HeadLayer):
         k = int(top_k)
         if not 0 <= k <= min(_b.LORA_HEAD_MAX_TOP, self.W.N):
             raise ValueError(f"top_k must be between 0 and {min(_b.LORA_HEAD_MAX_TOP, self.W.N)}")
-        with self._on(X, stream, ids) as handle:
+
+        def call(handle):
             f32 = torch.float32
             out = TokenLogProbs(
                 None if ids is None else torch.empty(ids.shape, dtype=f32, device=dev),
@@ -171,10 +182,12 @@ class LoraTokenLogProbs(_HeadLayer):
                 torch.empty((M, k), dtype=torch.int32, device=dev) if k else None,
                 torch.empty((M, k), dtype=f32, device=dev) if k else None,
                 self._saved(M, n, dev) if save else None)
-            ws = self._workspace(_b.head_fwd_workspace_bytes(M, self.W.K, self.W.N, n, k), dev, handle)
+            ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, k), dev, handle)
             _b.lora_logprob_fwd(X, M, self.W, ids, n, self.ignore_index, self.scale, k, out.logprob, out.entropy,
                                 out.lse, out.top_ids, out.top_logprob, out.saved, ws, stream=handle)
-        return out
+            return out
+
+        return self._run(call, X, stream, ids)
 
     def backward(self, X: torch.Tensor, ids: torch.Tensor | None, fwd: TokenLogProbs,
                  dlogprob: torch.Tensor | None = None, dentropy: torch.Tensor | None = None, dX=None,
@@ -190,13 +203,16 @@ class LoraTokenLogProbs(_HeadLayer):
                 raise ValueError("dentropy needs a forward with entropy=True")
             self._like(dentropy, "dentropy", torch.float32, (M,), dev)
         self._like(fwd.lse, "the forward's lse", torch.float32, (M,), dev)
-        with self._on(X, stream, ids, dlogprob, dentropy, fwd.lse, fwd.entropy, fwd.saved) as handle:
-            dX = self._dX(dX, X)
+
+        def call(handle):
+            out = self._dX(dX, X)
             saved, fwd.saved = fwd.saved, None  # the backward overwrites it
             ws = self._bwd_workspace(M, n, saved, dev, handle)
             _b.lora_logprob_bwd(X, M, self.W, ids, n, self.ignore_index, self.scale, fwd.lse, fwd.entropy, dlogprob,
-                                dentropy, saved, dX, ws, stream=handle)
-        return dX
+                                dentropy, saved, out, ws, stream=handle)
+            return out
+
+        return self._run(call, X, stream, ids, dlogprob, dentropy, fwd.lse, fwd.entropy, fwd.saved)
 
 
 class LoraDistill(_HeadLayer):
@@ -220,13 +236,16 @@ class LoraDistill(_HeadLayer):
                 stream=None) -> DistillLoss:
         M, dev = self._hidden(X), X.device
         n = self._teacher(ids, teacher_logits, M, dev)
-        with self._on(X, stream, ids, teacher_logits) as handle:
+
+        def call(handle):
             out = DistillLoss(torch.empty(M, dtype=torch.float32, device=dev),
                               torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, n, dev) if save else None)
-            ws = self._workspace(_b.head_fwd_workspace_bytes(M, self.W.K, self.W.N, n), dev, handle)
+            ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, 0), dev, handle)
             _b.lora_distill_fwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, out.loss, out.lse,
                                 out.saved, ws, stream=handle)
-        return out
+            return out
+
+        return self._run(call, X, stream, ids, teacher_logits)
 
     def backward(self, X: torch.Tensor, ids: torch.Tensor, teacher_logits: torch.Tensor, fwd: DistillLoss,
                  dloss: torch.Tensor, dX=None, stream=None) -> torch.Tensor:
@@ -234,10 +253,13 @@ class LoraDistill(_HeadLayer):
         n = self._teacher(ids, teacher_logits, M, dev)
         self._like(dloss, "dloss", torch.float32, (M,), dev)
         self._like(fwd.lse, "the forward's lse", torch.float32, (M,), dev)
-        with self._on(X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved) as handle:
-            dX = self._dX(dX, X)
+
+        def call(handle):
+            out = self._dX(dX, X)
             saved, fwd.saved = fwd.saved, None  # the backward overwrites it
             ws = self._bwd_workspace(M, n, saved, dev, handle)
             _b.lora_distill_bwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, fwd.lse, dloss,
-                                saved, dX, ws, stream=handle)
-        return dX
+                                saved, out, ws, stream=handle)
+            return out
+
+        return self._run(call, X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved)
