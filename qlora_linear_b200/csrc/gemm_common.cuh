@@ -24,8 +24,33 @@ struct HeadArgs {
   const float4* rowp;        // backward: [M] (lse / ln 2, Σc + g_H·H, g_H·ln 2, -)
   const float* rowf;         // EPI_HEAD_DX: [M] factors of the rows, or null
   int tiles;                 // 128-column tiles of the vocabulary
-  int rows;                  // M
+  // Rows that were compacted (head_compact_kernel): their number, and the caller's row of each.
+  // Null: all M rows in place.
+  const int* m_dev;
+  const int32_t* rowmap;
 };
+
+// Splits of the dX GEMM's reduction over the vocabulary: its output has few tiles (16 for up to
+// 256 rows of 4096) for 74 CTA pairs.  The cost in sixteenths of a fill of a pair: waves × (the
+// longest piece's fills + 6 for the pipeline's start and the extra epilogue), plus the pieces
+// written and read back, 2 × 256 KB each, at the 4.3 TB/s that leaves room for the operands, a
+// fill being 0.80 us (256 × 256 × 128 at a 74th of 1.55 PFLOP/s).  2048 rows, V = 128256,
+// D = 4096: 128 tiles in 4 pieces, 6.92 waves.
+constexpr int kHeadMaxSplits = 64, kHeadPairs = 74;
+__host__ __device__ inline int head_dx_splits(int tiles, int L, int max_units) {
+  int best = 1;
+  long long best_cost = 0;
+  for (int s = 1; s <= kHeadMaxSplits && s <= L && (s == 1 || static_cast<long long>(tiles) * s <= max_units); ++s) {
+    const long long units = static_cast<long long>(tiles) * s;
+    const long long cost = (units + kHeadPairs - 1) / kHeadPairs * ((L + s - 1) / s + 6) * 16 +
+                           (s > 1 ? units * 39 / 16 + 64 : 0);
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
 
 struct PairParams {
   int M;               // rows of Aop / out
@@ -65,7 +90,8 @@ struct PairParams {
   int sk_on;
   int sk_dp_tiles;
   float* kpart;
-  int splits;              // EPI_HEAD_DX: every tile's fills in this many pieces (see UnitWalk)
+  int splits;              // EPI_HEAD_DX: every tile's fills in this many pieces (see UnitWalk);
+  int max_units;           // chosen in the kernel, at most max_units pieces, when rows were compacted
   uint32_t* status;    // device status word, may be null
   uint64_t wait_ns;    // bound of every mbarrier wait
   // quantized weights only

@@ -100,12 +100,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
-  const int num_m = (p.M + C::BM - 1) / C::BM;
+  // rows of compacted operands are counted on the device
+  const bool counted = (EPI == EPI_HEAD_FWD || EPI == EPI_HEAD_DX) && p.head.m_dev != nullptr;
+  const int M = counted ? min(p.M, *p.head.m_dev) : p.M;
+  const int num_m = (M + C::BM - 1) / C::BM;
   const int num_n = (p.Nout + EpiTile<EPI>::COLS - 1) / EpiTile<EPI>::COLS;
   const int ntiles = num_m * num_n;
   const bool sk = EPI == EPI_STORE && p.sk_on != 0;  // only the plain store epilogue runs stream-K
-  const int splits = EPI == EPI_HEAD_DX ? p.splits : 1;
   const int nkb = (p.Kred + C::BK - 1) / C::BK;
+  const int splits = EPI != EPI_HEAD_DX ? 1 : counted ? head_dx_splits(ntiles, nkb, p.max_units) : p.splits;
   const int n_ext = p.r > 0 ? 1 : 0;         // one fill holds the whole LoRA block (r <= 128)
   const int tile_fills = nkb + n_ext;        // fills per tile
   const int ext_atoms = p.r > 64 ? 2 : 1;   // 64-wide rank atoms actually loaded
@@ -156,7 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
         const int brow = pair_brow<EPI>(nb, rank, p);  // this CTA's rows of the B tile
         // checked build: the tile exists and starts inside the output (a CTA's half of a
         // ragged tile may lie wholly past M or N: its boxes are TMA zero fills)
-        if (!lora_check(mb < num_m && nb < num_n && mb * C::BM < p.M && nb * EpiTile<EPI>::COLS < p.Nout, wc)) {
+        if (!lora_check(mb < num_m && nb < num_n && mb * C::BM < M && nb * EpiTile<EPI>::COLS < p.Nout, wc)) {
           ok = false;
           break;
         }
@@ -272,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       int mb, nb;
       pair_tile_coords(t, num_m, num_n, p.group_m, mb, nb);
       const int row = mb * C::BM + static_cast<int>(rank) * C::HM + quarter * 32 + lane;
-      return row < p.M && nb * C::BN + ((warp - 2) >> 2) * kHeadTile < p.Nout ? row : -1;
+      return row < M && nb * C::BN + ((warp - 2) >> 2) * kHeadTile < p.Nout ? row : -1;
     };
     auto head_pos = [&](int t) {
       int mb, nb;
@@ -344,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
           uint32_t v[32];
           tmem_ld_32x32b_x32(tbase + c * 32, v);
           tmem_ld_wait();
-          if (row < p.M) {
+          if (row < M) {
             if (EPI == EPI_HEAD_DX && un.slot < 0 && p.head.rowf != nullptr) {
               // a row of factor 0 is 0 whatever its operand held
               const float f = p.head.rowf[row];
@@ -352,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
               for (int j = 0; j < 32; ++j) v[j] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(v[j]) * f);
             }
             if (un.slot >= 0) epi_slot_chunk<C::BM>(p, v, un.slot, row - mb * C::BM, c * 32);
-            else epi_store_chunk(p, v, row, col0);
+            else epi_store_chunk(p, v, counted && EPI == EPI_HEAD_DX ? p.head.rowmap[row] : row, col0);
           }
         }
       } else if constexpr (EPI == EPI_CE_LSE) {
@@ -430,13 +433,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       } else if constexpr (EPI == EPI_HEAD_FWD) {
         if (hcol < p.Nout)  // warp-uniform
           head_fwd_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), hcol / kHeadTile,
-                        p.head.tiles, row < p.M, row, first, p.Nout, tmE, staging, release);
+                        p.head.tiles, row < M, M, row, first, p.Nout, tmE, staging, release);
         else
           release();
       } else if constexpr (EPI == EPI_HEAD_DLOGITS) {
         if (hcol < p.Nout)  // warp-uniform
           head_dlogits_tile(p.head, tbase + half * kHeadTile, min(kHeadTile, p.Nout - hcol), p.v0 + hcol, hcol,
-                            row < p.M, row, first, tmE, staging, release);
+                            row < M, M, row, first, tmE, staging, release);
         else
           release();
       } else if constexpr (EPI == EPI_ACC_F32) {

@@ -210,7 +210,7 @@ __device__ __forceinline__ void head_store_bf16(const CUtensorMap& tm, uint32_t 
 // elsewhere).
 template <typename Release>
 __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase, int nv, int nt, int np, bool in,
-                                              int row, const HeadFirst& first, int V, const CUtensorMap& tm,
+                                              int M, int row, const HeadFirst& first, int V, const CUtensorMap& tm,
                                               uint32_t stage, Release release) {
   constexpr int NC = kHeadTile / 32;
   const size_t at = static_cast<size_t>(row) * np + nt;
@@ -252,7 +252,7 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
   const uint64_t c2 = pack_f32x2(h.c2, h.c2), mm = pack_f32x2(-m, -m), ff = pack_f32x2(f, f);
   uint64_t s[4] = {0, 0, 0, 0}, t[4] = {0, 0, 0, 0};
   const int lane = threadIdx.x & 31;
-  const bool some = row - lane < h.rows;  // warp-uniform: the warp has rows
+  const bool some = row - lane < M;  // warp-uniform: the warp has rows
   uint32_t va[32], vb[32];
   auto chunk = [&](const uint32_t (&v)[32], int c) {
     if ((hits >> c) & 1u) head_store_chunk(v, nv - c * 32, h.zlog + col0 + c * 32);
@@ -290,11 +290,11 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
 // dz of one accumulator tile of nv <= 128 columns in bf16 (recomputed logits).
 // rowp: (lse / ln 2, Σc + g_H·H, g_H·ln 2); x0: the tile's first column of the output.
 template <typename Release>
-__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, int x0, bool in, int row,
+__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, int x0, bool in, int M, int row,
                                                   HeadFirst f, const CUtensorMap& tm, uint32_t stage,
                                                   Release release) {
   const int lane = threadIdx.x & 31;
-  const bool some = row - lane < h.rows;  // warp-uniform: the warp has rows
+  const bool some = row - lane < M;  // warp-uniform: the warp has rows
   const int2* sorted = h.sorted + static_cast<size_t>(row) * h.n;
   const float4 rp = in ? h.rowp[row] : make_float4(0.f, 0.f, 0.f, 0.f);
   uint32_t va[32], vb[32];
@@ -388,6 +388,15 @@ struct HeadRowArgs {
   float* loss;             // distillation: [M]
   int32_t* top_ids;        // [M][k]
   float* top_logprob;      // [M][k]
+  // rows compacted by head_compact_kernel; else null.  The caller's arrays go by its rows, the
+  // scratch by compacted ones.
+  int* m_dev;              // their number
+  int32_t* rowmap;         // [M] the caller's row of each
+  int32_t* slot_of;        // [M] of the caller's rows, -1: left out
+  const __nv_bfloat16* X;  // [M][D]
+  __nv_bfloat16* Xc;       // [M][D] compacted
+  __nv_bfloat16* dX;       // backward: [M][D]
+  int D;
   // preparation
   int2* sorted;            // [M][n]
   uint8_t* first;          // [M][tiles + 1]: tokens before each 128-column tile
@@ -404,6 +413,44 @@ struct HeadRowArgs {
 
 constexpr int kHeadRowWarps = 4;
 
+// Distillation skips rows without an entry (prompts, padding): the others' hidden states are moved
+// together, their number counted on the device, and the GEMMs stop there.  A row's results do not
+// depend on its place, so the order in which blocks get theirs does not show.  Rows left out have
+// loss 0 (and lse 0).  One warp a row.
+constexpr int kCompactWarps = 8;
+__global__ void __launch_bounds__(32 * kCompactWarps) head_compact_kernel(const HeadRowArgs a) {
+  griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
+  __shared__ int base;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kCompactWarps + w;
+  bool any = false;
+  if (row < a.M)
+    for (int i = lane; i < a.n; i += 32) any |= a.ids[static_cast<size_t>(row) * a.n + i] != a.ignore;
+  any = __any_sync(0xffffffffu, any);
+  __shared__ int taken[kCompactWarps];
+  if (lane == 0) taken[w] = any;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int i = 0; i < kCompactWarps; ++i) {
+    before += i < w ? taken[i] : 0;
+    all += taken[i];
+  }
+  if (threadIdx.x == 0) base = all > 0 ? atomicAdd(a.m_dev, all) : 0;
+  __syncthreads();
+  if (row >= a.M) return;
+  const int slot = any ? base + before : -1;
+  if (lane == 0) {
+    a.slot_of[row] = slot;
+    if (any) a.rowmap[slot] = row;
+    else a.loss[row] = a.lse_out[row] = 0.0f;
+  }
+  if (!any) return;
+  const uint4* src = reinterpret_cast<const uint4*>(a.X + static_cast<size_t>(row) * a.D);
+  uint4* dst = reinterpret_cast<uint4*>(a.Xc + static_cast<size_t>(slot) * a.D);
+#pragma unroll 4
+  for (int i = lane; i < a.D / 8; i += 32) dst[i] = src[i];
+}
+
 // One warp a row.  Sorts the row's tokens by id (by counting the entries before each: n <=
 // 128 values in shared memory) with their position (forward) or coefficient (backward);
 // ignored and out-of-range entries go last as 0x7fffffff and match no column.  Clears the
@@ -419,8 +466,14 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
   __shared__ int sid[kHeadRowWarps][kHeadMaxIds], ordered[kHeadRowWarps][kHeadMaxIds];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kHeadRowWarps + w;
-  if (row >= a.M) return;  // whole warps
+  const int slot = blockIdx.x * kHeadRowWarps + w;
+  if (slot >= a.M) return;  // whole warps
+  if (BWD && a.m_dev != nullptr && a.slot_of[slot] < 0) {  // the caller's row of this number was left out
+    uint4* d = reinterpret_cast<uint4*>(a.dX + static_cast<size_t>(slot) * a.D);
+    for (int i = lane; i < a.D / 8; i += 32) d[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (a.m_dev != nullptr && slot >= *a.m_dev) return;
+  const int row = a.m_dev != nullptr ? a.rowmap[slot] : slot;
   const int32_t* ids = a.ids + static_cast<size_t>(row) * a.n;
   float coef[kHeadPerLane];
   float csum = 0.0f;
@@ -447,13 +500,15 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
     for (int u = 0; u < kHeadPerLane; ++u) cabs += fabsf(coef[u]);
     cabs = warp_sum(cabs);
     if (lane == 0) {
-      const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f, lse = a.lse[row];
-      a.rowp[row] = make_float4(lse * kLog2e, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh * kLn2, 0.0f);
+      const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+      // without a gradient: probabilities of 0, whatever the logits
+      const float lse = gh == 0.0f && cabs == 0.0f ? INFINITY : a.lse[row];
+      a.rowp[slot] = make_float4(lse * kLog2e, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh * kLn2, 0.0f);
       if (a.rowf != nullptr) {
         float f = -a.scale * csum * expf(-lse);
         if (!(gh == 0.0f && lse >= -20.0f && lse <= 60.0f && fabsf(csum) >= cabs * 0x1p-6f && fabsf(f) > 1e-30f)) f = 1.0f;
         if (gh == 0.0f && cabs == 0.0f) f = 0.0f;
-        a.rowf[row] = f;
+        a.rowf[slot] = f;
       }
     }
   }
@@ -470,15 +525,15 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
       int before = 0;
       for (int j = 0; j < a.n; ++j) before += sid[w][j] < id || (sid[w][j] == id && j < i);
       ordered[w][before] = id;
-      a.sorted[static_cast<size_t>(row) * a.n + before] = make_int2(id, BWD ? __float_as_int(coef[u]) : i);
+      a.sorted[static_cast<size_t>(slot) * a.n + before] = make_int2(id, BWD ? __float_as_int(coef[u]) : i);
       if (BWD && a.sorted_logit != nullptr)
-        a.sorted_logit[static_cast<size_t>(row) * a.n + before] = a.id_logit[static_cast<size_t>(row) * a.n + i];
+        a.sorted_logit[static_cast<size_t>(slot) * a.n + before] = a.id_logit[static_cast<size_t>(slot) * a.n + i];
     }
   }
   __syncwarp();
   if (a.first != nullptr) {
     const int tiles = (a.V + kHeadTile - 1) / kHeadTile;
-    uint8_t* first = a.first + static_cast<size_t>(row) * tiles;
+    uint8_t* first = a.first + static_cast<size_t>(slot) * tiles;
     for (int t = lane; t < tiles; t += 32) {
       int lo = 0, hi = a.n;
       while (lo < hi) {
@@ -489,7 +544,7 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
       first[t] = static_cast<uint8_t>(lo);
     }
   }
-  if (!BWD && a.bound != nullptr && lane < a.kp) a.bound[static_cast<size_t>(row) * a.kp + lane] = 0u;
+  if (!BWD && a.bound != nullptr && lane < a.kp) a.bound[static_cast<size_t>(slot) * a.kp + lane] = 0u;
 }
 
 // First vocabulary entry of CTA i of head_rows_kernel: ranges of multiples of 16.
@@ -502,9 +557,10 @@ __host__ __device__ __forceinline__ int hr_first(int V, int i, int ctas) {
 __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const HeadRowArgs a) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kHeadRowWarps + w;
-  if (row >= a.M) return;  // whole warps
-  const float4* part = a.part + static_cast<size_t>(row) * a.np;
+  const int slot = blockIdx.x * kHeadRowWarps + w;
+  if (slot >= (a.m_dev != nullptr ? *a.m_dev : a.M)) return;  // whole warps
+  const int row = a.m_dev != nullptr ? a.rowmap[slot] : slot;
+  const float4* part = a.part + static_cast<size_t>(slot) * a.np;
   float m = -INFINITY;
   for (int i = lane; i < a.np; i += 32) m = fmaxf(m, part[i].x);
   m = warp_max(m) * a.c2;
@@ -533,7 +589,7 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
     if (i < a.n) {
       const int id = ids[i];
       if (id != a.ignore)
-        lp[u] = id >= 0 && id < a.V ? fmaf(a.id_logit[static_cast<size_t>(row) * a.n + i], a.c2, -m) * kLn2 - ls : NAN;
+        lp[u] = id >= 0 && id < a.V ? fmaf(a.id_logit[static_cast<size_t>(slot) * a.n + i], a.c2, -m) * kLn2 - ls : NAN;
       if (a.logprob != nullptr) a.logprob[static_cast<size_t>(row) * a.n + i] = lp[u];
     }
   }
@@ -757,6 +813,7 @@ constexpr int kSavedThreads = 256;
 __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const HeadArgs h, int V, int np) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
   const int row = blockIdx.x, tid = threadIdx.x;
+  if (h.m_dev != nullptr && row >= *h.m_dev) return;
   const float f = h.rowf[row];
   if (f == 0.0f) return;
   const float4 rp = h.rowp[row];

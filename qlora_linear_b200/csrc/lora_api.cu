@@ -627,7 +627,7 @@ lora_status_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUte
                           const PairParams& p, int sms, cudaStream_t st) {
   using C = PairCfg<B_MN>;
   const long long tiles = static_cast<long long>(cdiv(p.M, C::BM)) * cdiv(p.Nout, EpiTile<EPI>::COLS);
-  const long long units = EPI == EPI_HEAD_DX ? tiles * p.splits : tiles;
+  const long long units = EPI != EPI_HEAD_DX ? tiles : p.head.m_dev ? sms / 2 : tiles * p.splits;
   const long long pairs = p.sk_on ? kGemmPairs : (units < sms / 2 ? units : sms / 2);
   const int grid = static_cast<int>(2 * (pairs > 0 ? pairs : 1));
   {
@@ -1208,14 +1208,16 @@ inline int pow2_at_least(int k) {
 
 // Forward scratch: the batch's sorted tokens, their logits, the bounds, the partials of every
 // row and tile (or CTA), the chunks' maxima and the logits kept.  Pure functions of the sizes.
+size_t head_map_bytes(long long M) { return 256 + 2 * align256(static_cast<size_t>(M) * 4); }
 struct HeadFwdLayout {
-  bool few = false;
+  bool few = false, compact = false;
   long long chunk = 0;  // rows
   int np = 0;           // partials a row
   int ctas = 0, cpp = 0;  // few rows: CTAs; chunks a CTA or partial
-  size_t sorted_off = 0, logit_off = 0, first_off = 0, bound_off = 0, part_off = 0, cmax_off = 0, zlog_off = 0, total = 0;
+  size_t sorted_off = 0, logit_off = 0, first_off = 0, bound_off = 0, part_off = 0, cmax_off = 0, zlog_off = 0;
+  size_t map_off = 0, xc_off = 0, total = 0;
 };
-HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save) {
+HeadFwdLayout head_fwd_layout(long long M, long long D, long long V, int n, int k, bool save) {
   HeadFwdLayout l;
   const int kp = k > 0 ? pow2_at_least(k) : 0;
   l.few = M <= kHeadFewRows && !save;
@@ -1236,37 +1238,33 @@ HeadFwdLayout head_fwd_layout(long long M, long long V, int n, int k, bool save)
   l.part_off = l.bound_off + align256(R * kp * 4);
   l.cmax_off = l.part_off + align256(R * l.np * 16);
   l.zlog_off = l.cmax_off + align256(R * maxima);
-  l.total = l.zlog_off + align256(R * logits);
+  l.map_off = l.zlog_off + align256(R * logits);
+  l.total = l.map_off;
+  // compacted rows (distillation, in one batch, where fewer rows can mean fewer tiles): their map
+  // and hidden states
+  l.compact = M > 256 && n > 0 && k == 0 && l.chunk == M;
+  if (l.compact) {
+    l.xc_off = l.map_off + head_map_bytes(M);
+    l.total = l.xc_off + align256(R * D * 2);
+  }
   return l;
 }
 
-// Splits of the dX GEMM's reduction over the vocabulary (one wave of CTA pairs runs `pairs`
-// units, and its output has few tiles: 16 for up to 256 rows of 4096).  The cost in fills of a
-// pair: waves × (the longest piece's fills + 6 for the pipeline's start and the extra epilogue),
-// plus the pieces written and read back, 2 × 256 KB each, at the 4.3 TB/s that leaves room for
-// the operands, a fill being 0.80 us (256 × 256 × 128 at a 74th of 1.55 PFLOP/s).
-// A pure function of the sizes.  2048 rows, V = 128256, D = 4096: 128 tiles in 4 pieces, 6.92
-// waves.
-constexpr int kHeadMaxSplits = 64;
-int head_dx_splits(long long M, long long D, long long V) {
-  const long long tiles = static_cast<long long>(cdiv(M, 256)) * cdiv(D, 256);
-  const long long L = cdiv(V, 128);
-  int best = 1;
-  double best_cost = 0.0;
-  for (int s = 1; s <= kHeadMaxSplits && s <= L; ++s) {
-    const double waves = static_cast<double>((tiles * s + kGemmPairs - 1) / kGemmPairs);
-    const double slots = s > 1 ? double(tiles) * s * 2 * 262144 / 4.3e12 / 0.80e-6 + 4.0 : 0.0;
-    const double cost = waves * (static_cast<double>((L + s - 1) / s) + 6.0) + slots;
-    if (s == 1 || cost < best_cost) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return best;
+// Pieces of the dX GEMM (EPI_HEAD_DX) and the room for them: those of all M rows, and for fewer,
+// compacted rows up to four units a CTA pair.
+int head_dx_tiles(long long M, long long D) { return cdiv(M, 256) * cdiv(D, 256); }
+int head_dx_splits_of(long long M, long long D, long long V) {
+  return head_dx_splits(head_dx_tiles(M, D), cdiv(V, 128), 0x7fffffff);
+}
+int head_dx_units(long long M, long long D, long long V) {
+  const long long tiles = head_dx_tiles(M, D), L = cdiv(V, 128);
+  const int s = head_dx_splits_of(M, D, V);
+  const long long most = tiles * (L < kHeadMaxSplits ? L : kHeadMaxSplits), few = most < 4 * kHeadPairs ? most : 4 * kHeadPairs;
+  const long long all = s > 1 ? tiles * s : 0;
+  return static_cast<int>(all > few ? all : few);
 }
 size_t head_dx_slot_bytes(long long M, long long D, long long V) {
-  const int s = head_dx_splits(M, D, V);
-  return s > 1 ? static_cast<size_t>(cdiv(M, 256)) * cdiv(D, 256) * s * 262144 : 0;
+  return static_cast<size_t>(head_dx_units(M, D, V)) * 262144;
 }
 
 // Backward scratch: sorted (id, coefficient) pairs with their logits, the tiles' first of them,
@@ -1294,6 +1292,16 @@ HeadBwdLayout head_bwd_layout(long long M, long long D, long long V, int n) {
 inline size_t head_tau_off(long long M, long long V) { return align256(static_cast<size_t>(M) * V * 2); }
 inline size_t head_saved_logit_off(long long M, long long V) {
   return head_tau_off(M, V) + align256(static_cast<size_t>(M) * cdiv(V, kHeadTile) * 4);
+}
+
+inline size_t head_saved_map_off(long long M, long long V, int n) {
+  return head_saved_logit_off(M, V) + align256(static_cast<size_t>(M) * n * 4);
+}
+// The map of compacted rows: their number, the caller's row of each, and back.
+void head_set_map(HeadRowArgs& r, uint8_t* map, long long M) {
+  r.m_dev = reinterpret_cast<int*>(map);
+  r.rowmap = reinterpret_cast<int32_t*>(map + 256);
+  r.slot_of = reinterpret_cast<int32_t*>(map + 256 + align256(static_cast<size_t>(M) * 4));
 }
 
 bool head_sizes_ok(long long M, long long D, long long V, int n, int k) {
@@ -1336,7 +1344,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
                             void* workspace, size_t ws_bytes, cudaStream_t st) {
   const long long V = W->N, D = W->K;
   const int n = r.n, k = r.k;
-  const HeadFwdLayout l = head_fwd_layout(M, V, n, k, saved != nullptr);
+  const HeadFwdLayout l = head_fwd_layout(M, D, V, n, k, saved != nullptr);
   TRY(head_workspace(workspace, ws_bytes, l.total));
   DevInfo* dev = nullptr;
   TRY(dev_info(&dev));
@@ -1390,9 +1398,22 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     r.M = p.M;
     return launch_head_finalize(r, st);
   }
+  const bool compact = l.compact && r.loss != nullptr;
+  if (compact) {
+    head_set_map(r, saved ? static_cast<uint8_t*>(saved) + head_saved_map_off(M, V, n) : ws + l.map_off, M);
+    r.X = static_cast<const __nv_bfloat16*>(X);
+    r.Xc = reinterpret_cast<__nv_bfloat16*>(ws + l.xc_off);
+    r.D = static_cast<int>(D);
+    r.M = static_cast<int>(M);
+    h.m_dev = r.m_dev;
+    if (cudaMemsetAsync(r.m_dev, 0, sizeof(int), st) != cudaSuccess) return LORA_ERR_CUDA;
+    launch_k(head_compact_kernel, dim3(cdiv(M, kCompactWarps)), dim3(32 * kCompactWarps), 0, st, r);
+    count_launch();
+    TRY(last_launch());
+  }
   for (long long m0 = 0; m0 < M; m0 += l.chunk) {
     const long long m = M - m0 < l.chunk ? M - m0 : l.chunk;
-    const uint8_t* Xc = static_cast<const uint8_t*>(X) + static_cast<size_t>(m0) * D * 2;
+    const uint8_t* Xc = compact ? ws + l.xc_off : static_cast<const uint8_t*>(X) + static_cast<size_t>(m0) * D * 2;
     HeadRowArgs a = r;
     a.M = static_cast<int>(m);
     auto at = [&](auto* p, long long per) { return p ? p + m0 * per : p; };
@@ -1421,7 +1442,6 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     TRY(tmap_bf16(&tx, Xc, D, m, kBoxX, kBoxY));
     PairParams p = ce_params(m, V, D, nullptr, status, W);
     p.head = hc;
-    p.head.rows = p.M;
     CUtensorMap te = tx;  // not used unless e^z is kept
     if (saved) TRY(tmap_staged(&te, hc.expz, V, m));
     TRY((launch_gemm_w<false, EPI_HEAD_FWD>(W, tx, te, FSpec{Xc, static_cast<uint64_t>(D), static_cast<uint64_t>(m)}, p,
@@ -1460,6 +1480,11 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
     r.id_logit = reinterpret_cast<const float*>(sv + head_saved_logit_off(M, V));
     r.sorted_logit = reinterpret_cast<float*>(ws + l.logit_off);
     r.rowf = reinterpret_cast<float*>(ws + l.rowf_off);
+    if (r.teacher && head_fwd_layout(M, D, V, n, 0, true).compact) {
+      head_set_map(r, sv + head_saved_map_off(M, V, n), M);
+      r.dX = static_cast<__nv_bfloat16*>(dX);
+      r.D = static_cast<int>(D);
+    }
   } else if (n > 0) {
     r.first = ws + l.first_off;
   }
@@ -1473,6 +1498,8 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
   h.sorted = r.sorted;
   h.rowp = r.rowp;
   h.rowf = r.rowf;
+  h.m_dev = r.m_dev;
+  h.rowmap = r.rowmap;
   h.first = ws + l.first_off;
   h.tiles = tiles;
   CUtensorMap tx;
@@ -1497,7 +1524,6 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
       PairParams p = ce_params(M, w, D, dz, status, &Wc);
       p.v0 = static_cast<int>(v0);
       p.head = h;
-      p.head.rows = p.M;
       CUtensorMap te;
       TRY(tmap_staged(&te, dz, w, M));
       TRY((launch_gemm_w<false, EPI_HEAD_DLOGITS>(
@@ -1508,14 +1534,16 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
     const FSpec fs{dz, static_cast<uint64_t>(w), static_cast<uint64_t>(M)};
     PairParams q = ce_params(M, D, w, dX, status, &Wc);
     if (whole) {
-      q.splits = head_dx_splits(M, D, V);
+      q.splits = head_dx_splits_of(M, D, V);
+      q.max_units = head_dx_units(M, D, V);
       q.kpart = reinterpret_cast<float*>(ws + l.slot_off);
-      q.head.rowf = r.rowf;
+      q.head.rowf = h.rowf;
+      q.head.m_dev = h.m_dev;
+      q.head.rowmap = h.rowmap;
       TRY((launch_gemm_w<true, EPI_HEAD_DX>(&Wc, ta, ta, fs, q, dev->sms, st)));
-      if (q.splits > 1) {
-        const int num_m = cdiv(M, 256), num_n = cdiv(D, 256);
-        launch_k(splits_sum_kernel, dim3(num_m * num_n, 32), dim3(256), 0, st, q.kpart, q.out, q.M, q.Nout, num_m,
-                 num_n, q.group_m, q.splits, q.head.rowf);
+      if (q.splits > 1 || h.m_dev) {
+        launch_k(splits_sum_kernel, dim3(head_dx_tiles(M, D), 32), dim3(256), 0, st, q.kpart, q.out, q.M, q.Nout,
+                 q.group_m, q.splits, cdiv(V, 128), q.max_units, q.head);
         count_launch();
         TRY(last_launch());
       }
@@ -1815,7 +1843,7 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
 size_t lora_head_fwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n, int32_t k) {
   if (!head_sizes_ok(M, D, V, n, k)) return 0;
   // a forward with a saved buffer never takes the few-rows kernel: room for either
-  const size_t a = head_fwd_layout(M, V, n, k, false).total, b = head_fwd_layout(M, V, n, k, true).total;
+  const size_t a = head_fwd_layout(M, D, V, n, k, false).total, b = head_fwd_layout(M, D, V, n, k, true).total;
   return a > b ? a : b;
 }
 
@@ -1829,8 +1857,7 @@ size_t lora_head_bwd_workspace_bytes(int64_t M, int64_t D, int64_t V, int32_t n,
 
 size_t lora_head_saved_bytes(int64_t M, int64_t V, int32_t n) {
   if (!head_sizes_ok(M, 8, V, n, 0)) return 0;
-  const size_t b = head_saved_logit_off(M, V) + align256(static_cast<size_t>(M) * n * 4);
-  return b > 0 ? b : 256;  // 0 stands for invalid sizes
+  return head_saved_map_off(M, V, n) + head_map_bytes(M);
 }
 
 lora_status_t lora_logprob_fwd(const void* X, int64_t M, const lora_weight_t* W, const int32_t* ids, int32_t n,

@@ -55,12 +55,18 @@ __global__ void __launch_bounds__(256) streamk_fixup_kernel(const float* __restr
       make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
 }
 
-// The second kernel of a launch with splits: out = the pieces of every tile added in order of
-// their depth, times the row's factor (rowf may be null).  Block (x, y): rows [8y, 8y + 8) of tile x; thread (row, 8-column chunk).
+// The second kernel of a dX launch with splits: out = the pieces of every tile added in order of
+// their depth, times the row's factor (h.rowf may be null).  Block (x, y): rows [8y, 8y + 8) of tile
+// x; thread (row, 8-column chunk).  Compacted rows are counted and split as in the GEMM.
 __global__ void __launch_bounds__(256) splits_sum_kernel(const float* __restrict__ kpart, __nv_bfloat16* __restrict__ out,
-                                                         int M, int Nout, int num_m, int num_n, int group_m, int splits,
-                                                         const float* __restrict__ rowf) {
+                                                         int M, int Nout, int group_m, int splits, int fills,
+                                                         int max_units, const HeadArgs h) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
+  if (h.m_dev != nullptr) M = min(M, *h.m_dev);
+  const int num_m = (M + 255) / 256, num_n = (Nout + 255) / 256, tiles = num_m * num_n;
+  if (static_cast<int>(blockIdx.x) >= tiles) return;
+  if (h.m_dev != nullptr) splits = head_dx_splits(tiles, fills, max_units);
+  if (splits == 1) return;  // the GEMM wrote the output
   int mb, nb;
   pair_tile_coords(blockIdx.x, num_m, num_n, group_m, mb, nb);
   const int lr = blockIdx.y * 8 + (threadIdx.x >> 5), lc = (threadIdx.x & 31) * 8;
@@ -70,17 +76,18 @@ __global__ void __launch_bounds__(256) splits_sum_kernel(const float* __restrict
 #pragma unroll 4
   for (int s = 0; s < splits; ++s) {
     const float4* q = reinterpret_cast<const float4*>(
-        kpart + ((static_cast<size_t>(s) * gridDim.x + blockIdx.x) * 256 + lr) * 256 + lc);
+        kpart + ((static_cast<size_t>(s) * tiles + blockIdx.x) * 256 + lr) * 256 + lc);
     const float4 x = q[0], y = q[1];
     a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
     a[4] += y.x; a[5] += y.y; a[6] += y.z; a[7] += y.w;
   }
-  if (rowf != nullptr) {
-    const float f = rowf[row];  // a row of factor 0 is 0 whatever its operand held
+  if (h.rowf != nullptr) {
+    const float f = h.rowf[row];  // a row of factor 0 is 0 whatever its operand held
 #pragma unroll
     for (int j = 0; j < 8; ++j) a[j] = f == 0.0f ? 0.0f : a[j] * f;
   }
-  *reinterpret_cast<uint4*>(out + static_cast<size_t>(row) * Nout + col) =
+  const int orow = h.m_dev != nullptr ? h.rowmap[row] : row;
+  *reinterpret_cast<uint4*>(out + static_cast<size_t>(orow) * Nout + col) =
       make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));
 }
 

@@ -142,6 +142,32 @@ def test_distillation(lib, M, D, V, n, T):
     assert layer.status() == lib.LORA_OK
 
 
+@pytest.mark.parametrize("kept", ["none", "one", "last", "every_third", "all_but_first_block"])
+def test_distillation_of_few_rows_of_a_batch(lib, kept):
+    """Rows without an entry cost nothing (they are left out of the products) and change nothing:
+    prompts in front, padding behind, rows in between, a batch of nothing else."""
+    M, D, V, n = 1100, 136, 1032, 5
+    inp = make_head_case(HeadCase("few", M, D, V, n, 171, ignore_frac=0.05))
+    keep = np.zeros(M, dtype=bool)
+    keep[{"none": slice(0, 0), "one": slice(700, 701), "last": slice(M - 3, M), "every_third": slice(0, M, 3),
+          "all_but_first_block": slice(256, M)}[kept]] = True
+    inp["ids"][~keep] = -100
+    X, W = O.bf16_to_f64(inp["X"]), O.bf16_to_f64(inp["W"])
+    ref = O.distill(X, W, inp["ids"], inp["teacher"], -100, 1.0, inp["dloss"])
+    layer = head(lib, inp, lib.LoraDistill)
+    x = dev_bf16(inp["X"])
+    x[torch.from_numpy(~keep).cuda()] = float("nan")  # whatever those rows hold
+    ids, t, dl = up(inp, "ids", "teacher", "dloss")
+    for save in (False, True, True):
+        out = layer.forward(x, ids, t, save=save)
+        close("loss", out.loss, ref["loss"], LOSS_ATOL)
+        if save:
+            dX = layer.backward(x, ids, t, out, dl, dX=torch.full_like(x, 7.0))
+            check_dX(kept, dX, ref, W, 2.0 * inp["dloss"].astype(np.float64), 1.0)
+            assert np.all(host_f64(dX)[ref["q"].sum(1) == 0] == 0)
+    assert layer.status() == lib.LORA_OK
+
+
 @pytest.mark.parametrize("M", [3, 200])
 @pytest.mark.parametrize("kind", ["zero_rows", "repeated", "ascending", "descending", "block_of_best"])
 def test_alternatives_in_hard_orders(lib, M, kind):
