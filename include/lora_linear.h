@@ -340,7 +340,9 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
  *
  * Entries with ids_mi == ignore_index have logprob 0, no weight in q and no gradient
  * (ignore_index may be a valid id, which is then never counted); a row without any other has
- * loss 0 and a zero gradient, and so has a row whose listed teacher logits are all -inf.  An
+ * loss 0 and a zero gradient whatever its hidden state holds, and so has a row whose listed
+ * teacher logits are all -inf (their lse is unspecified).  lora_distill_fwd leaves rows without an
+ * entry out of its products.  An
  * id outside [0, V) that is not ignore_index gives a NaN logprob, and a NaN loss where its q is
  * not 0 (its gradient is unspecified).  An id listed twice counts twice.  A NaN or +inf
  * teacher logit gives that row a NaN loss.  Rows whose logits are not finite give NaN.
@@ -366,7 +368,8 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
  * dloss fp32 [M]; dX bf16 [M, D] (out).
  *
  * Workspace: lora_head_fwd_workspace_bytes(M, D, V, n, k) for the forward (k = 0 for
- * lora_distill_fwd); lora_head_bwd_workspace_bytes(M, D, V, n, slice) for the backward, slice
+ * lora_distill_fwd; up to 1.25 GiB with k > 0, whose rows go in batches, and room for a copy of X
+ * otherwise); lora_head_bwd_workspace_bytes(M, D, V, n, slice) for the backward, slice
  * = 0 with a saved forward, else the vocabulary rows a slice (V or more: all at once; fewer
  * than 256 columns' room is LORA_ERR_WORKSPACE).  One buffer may serve both; its first 256
  * bytes must be zero before its first use.  Limits as for the layer: D % 8 == 0, V % 8 == 0;

@@ -21,7 +21,7 @@ struct HeadArgs {
   const uint8_t* first;      // [M][tiles of the vocabulary] tokens before each tile
   __nv_bfloat16* expz;       // [M][V] 2^{y - tau}, or null
   float* tau;                // [M][tiles], with expz
-  const float4* rowp;        // backward: [M] (lse / ln 2, Σc + g_H·H, g_H·ln 2, -)
+  const float4* rowp;        // backward: [M] (lse / ln 2, Σc + g_H·H, g_H·ln 2, any gradient)
   const float* rowf;         // EPI_HEAD_DX: [M] factors of the rows, or null
   int tiles;                 // 128-column tiles of the vocabulary
   // Rows that were compacted (head_compact_kernel): their number, and the caller's row of each.

@@ -19,9 +19,9 @@
 // alternatives are kept as accumulators.
 //
 // The alternatives.  Every 32 columns (a chunk) leave their maximum, and (pair kernel) their 32
-// logits only if that reaches a lower bound of the row's k-th largest logit; head_finalize_top_kernel then
-// looks at the few chunks that reach the final bound.  The bound: cut what was seen so far into
-// kp >= k disjoint groups; the least of the groups' maxima is at most the k-th largest.  It
+// logits only if that reaches a lower bound of the row's k-th largest logit;
+// head_finalize_top_kernel then looks at the k best chunks.  The bound: cut what was seen so far
+// into kp >= k disjoint groups; the least of the groups' maxima is at most the k-th largest.  It
 // never falls, so a chunk that reaches a later bound has been written.  In random order about
 // k·log k chunks of the whole vocabulary reach it.
 #pragma once
@@ -287,11 +287,11 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
   if (keep) h.tau[at] = tau;
 }
 
-// dz of one accumulator tile of nv <= 128 columns in bf16 (recomputed logits).
-// rowp: (lse / ln 2, Σc + g_H·H, g_H·ln 2); x0: the tile's first column of the output.
+// dz of one accumulator tile of nv <= 128 columns in bf16 (recomputed logits).  rowp: (lse / ln 2,
+// Σc + g_H·H, g_H·ln 2, 0 for a row without a gradient); x0: the tile's first column of the output.
 template <typename Release>
-__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, int x0, bool in, int M, int row,
-                                                  HeadFirst f, const CUtensorMap& tm, uint32_t stage,
+__device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tbase, int nv, int v0, int x0, bool in,
+                                                  int M, int row, HeadFirst f, const CUtensorMap& tm, uint32_t stage,
                                                   Release release) {
   const int lane = threadIdx.x & 31;
   const bool some = row - lane < M;  // warp-uniform: the warp has rows
@@ -300,7 +300,10 @@ __device__ __forceinline__ void head_dlogits_tile(const HeadArgs& h, uint32_t tb
   uint32_t va[32], vb[32];
   auto chunk = [&](const uint32_t (&v)[32], int c) {
     float d[32];
-    if (rp.z == 0.0f) {
+    if (rp.w == 0.0f) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) d[j] = 0.0f;
+    } else if (rp.z == 0.0f) {
       const float w = -h.scale * rp.y;
 #pragma unroll
       for (int j = 0; j < 32; ++j) d[j] = w * ex2_approx(fmaf(__uint_as_float(v[j]), h.c2, -rp.x));
@@ -399,7 +402,7 @@ struct HeadRowArgs {
   int D;
   // preparation
   int2* sorted;            // [M][n]
-  uint8_t* first;          // [M][tiles + 1]: tokens before each 128-column tile
+  uint8_t* first;          // [M][tiles]: tokens before each 128-column tile
   float* sorted_logit;     // backward from a saved forward: [M][n] id_logit in sorted order
   float* rowf;             // backward from a saved forward: [M] see head_saved_rows_kernel
   unsigned* bound;         // [M][kp] or null
@@ -501,13 +504,14 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
     cabs = warp_sum(cabs);
     if (lane == 0) {
       const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
-      // without a gradient: probabilities of 0, whatever the logits
-      const float lse = gh == 0.0f && cabs == 0.0f ? INFINITY : a.lse[row];
-      a.rowp[slot] = make_float4(lse * kLog2e, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh * kLn2, 0.0f);
+      const bool none = gh == 0.0f && cabs == 0.0f;  // no gradient, whatever the logits
+      const float lse = none ? 0.0f : a.lse[row];
+      a.rowp[slot] = make_float4(lse * kLog2e, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh * kLn2,
+                                 none ? 0.0f : 1.0f);
       if (a.rowf != nullptr) {
         float f = -a.scale * csum * expf(-lse);
         if (!(gh == 0.0f && lse >= -20.0f && lse <= 60.0f && fabsf(csum) >= cabs * 0x1p-6f && fabsf(f) > 1e-30f)) f = 1.0f;
-        if (gh == 0.0f && cabs == 0.0f) f = 0.0f;
+        if (none) f = 0.0f;
         a.rowf[slot] = f;
       }
     }
@@ -855,7 +859,7 @@ __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const He
     for (int t = tid; t < np; t += kSavedThreads) {
       const float tt = tau[t];
       if (tt == 0.0f) continue;
-      const float es = exp2f(tt);  // tau < -43 here
+      const float es = exp2f(tt);  // at most 2^86.6, an lse of 60
       for (int col = t * kHeadTile; col < min(V, (t + 1) * kHeadTile); ++col)
         zrow[col] = __float2bfloat16_rn(__bfloat162float(zrow[col]) * es);
     }

@@ -1206,9 +1206,16 @@ inline int pow2_at_least(int k) {
   return p;
 }
 
+// The map of compacted rows: their number, the caller's row of each, and back.
+size_t head_map_bytes(long long M) { return 256 + 2 * align256(static_cast<size_t>(M) * 4); }
+void head_set_map(HeadRowArgs& r, uint8_t* map, long long M) {
+  r.m_dev = reinterpret_cast<int*>(map);
+  r.rowmap = reinterpret_cast<int32_t*>(map + 256);
+  r.slot_of = reinterpret_cast<int32_t*>(map + 256 + align256(static_cast<size_t>(M) * 4));
+}
+
 // Forward scratch: the batch's sorted tokens, their logits, the bounds, the partials of every
 // row and tile (or CTA), the chunks' maxima and the logits kept.  Pure functions of the sizes.
-size_t head_map_bytes(long long M) { return 256 + 2 * align256(static_cast<size_t>(M) * 4); }
 struct HeadFwdLayout {
   bool few = false, compact = false;
   long long chunk = 0;  // rows
@@ -1224,7 +1231,8 @@ HeadFwdLayout head_fwd_layout(long long M, long long D, long long V, int n, int 
   l.ctas = l.few ? hr_ctas(V) : 0;
   l.np = l.few ? l.ctas * HR_WARPS : cdiv(V, kHeadTile);
   l.cpp = l.few ? hr_chunks(V) : kHeadTile / 32;
-  const size_t maxima = k > 0 ? static_cast<size_t>(l.few ? l.ctas : l.np) * l.cpp * 4 : 0, logits = k > 0 ? static_cast<size_t>(V) * 4 : 0;
+  const size_t maxima = k > 0 ? static_cast<size_t>(l.few ? l.ctas : l.np) * l.cpp * 4 : 0;
+  const size_t logits = k > 0 ? static_cast<size_t>(V) * 4 : 0;
   const size_t first = n > 0 && !l.few ? cdiv(V, kHeadTile) : 0;
   const size_t per_row = 12 * static_cast<size_t>(n) + first + 4 * kp + 16 * static_cast<size_t>(l.np) + maxima + logits;
   long long c = static_cast<long long>(kHeadChunkBytes / per_row) / 256 * 256;
@@ -1259,7 +1267,8 @@ int head_dx_splits_of(long long M, long long D, long long V) {
 int head_dx_units(long long M, long long D, long long V) {
   const long long tiles = head_dx_tiles(M, D), L = cdiv(V, 128);
   const int s = head_dx_splits_of(M, D, V);
-  const long long most = tiles * (L < kHeadMaxSplits ? L : kHeadMaxSplits), few = most < 4 * kHeadPairs ? most : 4 * kHeadPairs;
+  const long long most = tiles * (L < kHeadMaxSplits ? L : kHeadMaxSplits);
+  const long long few = most < 4 * kHeadPairs ? most : 4 * kHeadPairs;
   const long long all = s > 1 ? tiles * s : 0;
   return static_cast<int>(all > few ? all : few);
 }
@@ -1267,12 +1276,12 @@ size_t head_dx_slot_bytes(long long M, long long D, long long V) {
   return static_cast<size_t>(head_dx_units(M, D, V)) * 262144;
 }
 
-// Backward scratch: sorted (id, coefficient) pairs with their logits, the tiles' first of them,
-// and the coefficients of all rows; then
-// either the pieces of a dX GEMM over the whole vocabulary with, unless the logits
-// were saved, dz [M, V] behind them, or the fp32 sum of dX with a slice of dz.
+// Backward scratch: sorted (id, coefficient) pairs with their logits, the tiles' first of them, and
+// the coefficients of all rows; then either the pieces of a dX GEMM over the whole vocabulary with,
+// unless the logits were saved, dz [M, V] behind them, or the fp32 sum of dX with a slice of dz.
 struct HeadBwdLayout {
-  size_t sorted_off = 0, logit_off = 0, first_off = 0, rowp_off = 0, rowf_off = 0, slot_off = 0, whole_dz_off = 0, acc_off = 0, slice_dz_off = 0;
+  size_t sorted_off = 0, logit_off = 0, first_off = 0, rowp_off = 0, rowf_off = 0;
+  size_t slot_off = 0, whole_dz_off = 0, acc_off = 0, slice_dz_off = 0;
 };
 HeadBwdLayout head_bwd_layout(long long M, long long D, long long V, int n) {
   HeadBwdLayout l;
@@ -1297,13 +1306,6 @@ inline size_t head_saved_logit_off(long long M, long long V) {
 inline size_t head_saved_map_off(long long M, long long V, int n) {
   return head_saved_logit_off(M, V) + align256(static_cast<size_t>(M) * n * 4);
 }
-// The map of compacted rows: their number, the caller's row of each, and back.
-void head_set_map(HeadRowArgs& r, uint8_t* map, long long M) {
-  r.m_dev = reinterpret_cast<int*>(map);
-  r.rowmap = reinterpret_cast<int32_t*>(map + 256);
-  r.slot_of = reinterpret_cast<int32_t*>(map + 256 + align256(static_cast<size_t>(M) * 4));
-}
-
 bool head_sizes_ok(long long M, long long D, long long V, int n, int k) {
   return M >= 0 && M <= (1LL << 31) - 256 && D > 0 && D <= (1LL << 30) && V > 0 && V <= (1LL << 30) && n >= 0 &&
          n <= kHeadMaxIds && k >= 0 && k <= kHeadMaxTop;

@@ -4,6 +4,7 @@ each with its gradient in the hidden states."""
 from __future__ import annotations
 
 import dataclasses
+import threading
 
 import torch
 
@@ -16,7 +17,7 @@ _current_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_s
 class TokenLogProbs:
     """What :meth:`LoraTokenLogProbs.forward` returns.  ``logprob`` has the shape of the ids
     given (None without ids); ``entropy`` [M]; ``lse`` [M]; ``top_ids`` int32 and
-    ``top_logprob`` [M, k] (None for k = 0).  ``saved`` belongs to the backward."""
+    ``top_logprob`` [M, k] (None for k = 0).  ``saved`` and ``tokens`` belong to the backward."""
 
     logprob: torch.Tensor | None
     lse: torch.Tensor
@@ -24,16 +25,18 @@ class TokenLogProbs:
     top_ids: torch.Tensor | None = None
     top_logprob: torch.Tensor | None = None
     saved: torch.Tensor | None = None
+    tokens: int = 0
 
 
 @dataclasses.dataclass
 class DistillLoss:
-    """What :meth:`LoraDistill.forward` returns: ``loss`` [M], ``lse`` [M]; ``saved`` belongs
-    to the backward."""
+    """What :meth:`LoraDistill.forward` returns: ``loss`` [M], ``lse`` [M]; ``saved`` and ``tokens``
+    belong to the backward."""
 
     loss: torch.Tensor
     lse: torch.Tensor
     saved: torch.Tensor | None = None
+    tokens: int = 0
 
 
 class _HeadLayer:
@@ -41,8 +44,8 @@ class _HeadLayer:
 
     A call runs on ``stream`` (default: the current stream of X's device) and takes its outputs
     and its workspace from that stream's memory, one workspace a stream, so calls on two streams
-    do not meet in it.  A call under CUDA graph capture takes a workspace of its own from the
-    graph's memory.
+    do not meet in it; a lock keeps two threads' calls on one stream apart.  A call under CUDA
+    graph capture takes a workspace of its own from the graph's memory.
     """
 
     def __init__(self, W: "_b.LoraWeight", ignore_index: int = -100, temperature: float = 1.0, slice_: int = 0):
@@ -54,12 +57,14 @@ class _HeadLayer:
         self.scale = 1.0 / float(temperature)
         self._ws = {}
         self._sizes = {}
+        self._lock = threading.Lock()
 
     def _run(self, call, X, stream, *inputs):
         """``call(handle)`` with X's device and ``stream`` current; returns what it returns."""
         index = X.device.index
         if stream is None and index == torch.cuda.current_device():
-            return call(_current_raw_stream(index))  # the usual case, without the context managers
+            with self._lock:
+                return call(_current_raw_stream(index))  # the usual case, without the context managers
         with torch.cuda.device(index):
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=X.device)
@@ -69,7 +74,7 @@ class _HeadLayer:
                 for t in (X, *inputs):
                     if t is not None:
                         t.record_stream(stream)
-            with torch.cuda.stream(stream):
+            with torch.cuda.stream(stream), self._lock:
                 return call(stream.cuda_stream)
 
     def _bytes(self, fn, *sizes) -> int:
@@ -142,6 +147,13 @@ class _HeadLayer:
     def _saved(self, M, n, device):
         return torch.empty(self._bytes(_b.head_saved_bytes, M, self.W.N, n), dtype=torch.uint8, device=device)
 
+    def _take_saved(self, fwd, M, n):
+        """The forward's saved buffer for this backward, which overwrites it (None: recompute)."""
+        saved, fwd.saved = fwd.saved, None
+        if saved is not None and (fwd.tokens != n or saved.numel() != self._bytes(_b.head_saved_bytes, M, self.W.N, n)):
+            raise ValueError("the forward was saved with other sizes (rows, tokens a row or vocabulary)")
+        return saved
+
     def _bwd_workspace(self, M, n, saved, device, handle):
         slice_ = 0 if saved is not None else self._slice(M)
         return self._workspace(self._bytes(_b.head_bwd_workspace_bytes, M, self.W.K, self.W.N, n, slice_), device, handle)
@@ -181,7 +193,7 @@ class LoraTokenLogProbs(_HeadLayer):
                 torch.empty(M, dtype=f32, device=dev) if entropy else None,
                 torch.empty((M, k), dtype=torch.int32, device=dev) if k else None,
                 torch.empty((M, k), dtype=f32, device=dev) if k else None,
-                self._saved(M, n, dev) if save else None)
+                self._saved(M, n, dev) if save else None, n)
             ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, k), dev, handle)
             _b.lora_logprob_fwd(X, M, self.W, ids, n, self.ignore_index, self.scale, k, out.logprob, out.entropy,
                                 out.lse, out.top_ids, out.top_logprob, out.saved, ws, stream=handle)
@@ -206,7 +218,7 @@ class LoraTokenLogProbs(_HeadLayer):
 
         def call(handle):
             out = self._dX(dX, X)
-            saved, fwd.saved = fwd.saved, None  # the backward overwrites it
+            saved = self._take_saved(fwd, M, n)
             ws = self._bwd_workspace(M, n, saved, dev, handle)
             _b.lora_logprob_bwd(X, M, self.W, ids, n, self.ignore_index, self.scale, fwd.lse, fwd.entropy, dlogprob,
                                 dentropy, saved, out, ws, stream=handle)
@@ -239,7 +251,7 @@ class LoraDistill(_HeadLayer):
 
         def call(handle):
             out = DistillLoss(torch.empty(M, dtype=torch.float32, device=dev),
-                              torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, n, dev) if save else None)
+                              torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, n, dev) if save else None, n)
             ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, 0), dev, handle)
             _b.lora_distill_fwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, out.loss, out.lse,
                                 out.saved, ws, stream=handle)
@@ -256,7 +268,7 @@ class LoraDistill(_HeadLayer):
 
         def call(handle):
             out = self._dX(dX, X)
-            saved, fwd.saved = fwd.saved, None  # the backward overwrites it
+            saved = self._take_saved(fwd, M, n)
             ws = self._bwd_workspace(M, n, saved, dev, handle)
             _b.lora_distill_bwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, fwd.lse, dloss,
                                 saved, out, ws, stream=handle)

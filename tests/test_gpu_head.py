@@ -447,6 +447,69 @@ def test_graphs_and_streams(lib):
     del graphs
 
 
+@pytest.mark.parametrize("M", [40, 250, 900])
+def test_rows_without_a_gradient_hold_anything(lib, M):
+    """NaN hidden states in rows that have no entry (or no upstream gradient) reach neither their own
+    nor another row's gradient, recomputed in one piece, in slices or from a saved forward."""
+    inp = make_head_case(HeadCase("pad", M, 64, 1000, 3, 181))
+    inp["ids"][::4] = -100
+    inp["dlogprob"][::4] = 0
+    off = (inp["ids"] == -100).all(1)
+    inp["dlogprob"][off] = 0
+    W = O.bf16_to_f64(inp["W"])
+    lr = O.token_logprobs(O.bf16_to_f64(inp["X"]), W, inp["ids"], -100, 1.0, 0, inp["dlogprob"])
+    kr = O.distill(O.bf16_to_f64(inp["X"]), W, inp["ids"], inp["teacher"], -100, 1.0, inp["dloss"])
+    x = dev_bf16(inp["X"])
+    x[torch.from_numpy(off).cuda()] = float("nan")
+    ids, t, dl, dlp = up(inp, "ids", "teacher", "dloss", "dlogprob")
+    for kw in ({}, {"slice_": 512}):
+        lp, kd = head(lib, inp, lib.LoraTokenLogProbs, **kw), head(lib, inp, lib.LoraDistill, **kw)
+        for save in (False, True):
+            o, d = lp.forward(x, ids, save=save), kd.forward(x, ids, t, save=save)
+            close("loss", d.loss, kr["loss"], LOSS_ATOL)
+            check_dX("logprob", lp.backward(x, ids, o, dlp), lr, W, grads(inp), 1.0, 2 if save else 1)
+            check_dX("distill", kd.backward(x, ids, t, d, dl), kr, W, 2.0 * inp["dloss"].astype(np.float64), 1.0)
+
+
+def test_same_bits_of_compacted_rows(lib):
+    """Distillation's rows find their places in any order; their results are the same bits."""
+    inp = make_head_case(HeadCase("order", 3000, 64, 1000, 4, 191, ignore_frac=1.0))
+    x = dev_bf16(inp["X"])
+    ids, t, dl = up(inp, "ids", "teacher", "dloss")
+    layer = head(lib, inp, lib.LoraDistill)
+    runs = []
+    for _ in range(4):
+        o = layer.forward(x, ids, t, save=True)
+        runs.append((o.loss, layer.backward(x, ids, t, o, dl)))
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(runs[0], r))
+
+
+def test_two_threads_on_one_stream(lib):
+    import threading
+
+    inp = make_head_case(HeadCase("threads", 300, 128, 3000, 4, 201))
+    x = dev_bf16(inp["X"])
+    ids, t, dl = up(inp, "ids", "teacher", "dloss")
+    layer = head(lib, inp, lib.LoraDistill)
+    xs = [x, x.flip(0).contiguous()]
+    want = [layer.forward(v, ids, t).loss for v in xs]
+    got = [[], []]
+
+    def work(i):
+        for _ in range(50):
+            o = layer.forward(xs[i], ids, t, save=True)
+            got[i].append((o.loss, layer.backward(xs[i], ids, t, o, dl)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(loss, want[i]) and torch.equal(dX, got[i][0][1]) for loss, dX in got[i])
+
+
 def test_layer_checks(lib):
     inp = make_head_case(HeadCase("chk", 8, 64, 256, 2, 151))
     lp, kd = head(lib, inp, lib.LoraTokenLogProbs), head(lib, inp, lib.LoraDistill)
@@ -463,6 +526,7 @@ def test_layer_checks(lib):
                  lambda: lp.backward(x, ids, o, dlp, torch.ones(8, device="cuda")),
                  lambda: lp.backward(x[:4], ids[:4], o, dlp[:4]),
                  lambda: lp.backward(x, ids, o, dlp, dX=torch.empty((8, 64), device="cuda")),
+                 lambda: lp.backward(x, ids[:, 0].contiguous(), lp.forward(x, ids, save=True)),
                  lambda: kd.forward(x, ids[:, 0].contiguous(), t), lambda: kd.forward(x, ids, t[:, :1]),
                  lambda: kd.forward(x, ids, t.double()), lambda: kd.forward(x, torch.zeros((8, 129), dtype=torch.int32,
                                                                                        device="cuda"), t)):
