@@ -12,7 +12,7 @@ struct HeadArgs {
   float scale, c2;           // scale, scale / ln 2
   int n;                     // given tokens a row
   const int2* sorted;        // [M][n] by id: (id, position) forward, (id, coefficient) backward
-  float* id_logit;           // accumulators of the given tokens, [M][n] by position; head_saved_rows_kernel: in sorted order
+  float* id_logit;           // forward: accumulators of the given tokens, [M][n] by position
   int k, kp;                 // alternatives a row, and the power of two >= k of their groups
   unsigned* bound;           // forward: [M][kp] group maxima over the tiles seen so far
   float* cmax;               // forward: [M][tiles · chunks] maxima of every 32 columns

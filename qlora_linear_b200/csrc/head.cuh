@@ -403,7 +403,6 @@ struct HeadRowArgs {
   // preparation
   int2* sorted;            // [M][n]
   uint8_t* first;          // [M][tiles]: tokens before each 128-column tile
-  float* sorted_logit;     // backward from a saved forward: [M][n] id_logit in sorted order
   float* rowf;             // backward from a saved forward: [M] see head_saved_rows_kernel
   unsigned* bound;         // [M][kp] or null
   float4* rowp;            // backward: [M]
@@ -454,39 +453,34 @@ __global__ void __launch_bounds__(32 * kCompactWarps) head_compact_kernel(const 
   for (int i = lane; i < a.D / 8; i += 32) dst[i] = src[i];
 }
 
-// One warp a row.  Sorts the row's tokens by id (by counting the entries before each: n <=
-// 128 values in shared memory) with their position (forward) or coefficient (backward);
-// ignored and out-of-range entries go last as 0x7fffffff and match no column.  Clears the
-// forward's bounds; writes the backward's row coefficients.
+// What the backward needs of a row besides its tokens.
+struct HeadRowGrad {
+  float4 rp;  // (lse / ln 2, Σc + g_H·H, g_H·ln 2, 0 for a row without a gradient)
+  float f;    // factor of a row from a saved forward, see head_saved_rows_kernel
+};
+
+// One warp sorts a row's tokens by id, by counting the entries before each (n <= 128 values in
+// shared memory): at(sorted index, id, position, coefficient) for every one; ignored and
+// out-of-range entries go last as 0x7fffffff and match no column.  The coefficients (backward) are
+// the upstream gradients c_i: dlogprob, or -dloss·q_i.
 //
-// rowf (backward from a saved forward): with g_H = 0 the row's dz is -scale·C·e^{-lse} (C = Σc)
-// times the saved e^z, but for its given tokens: that factor, if lse is within what e^z can hold
-// in bf16 ([-20, 60]: the maximum is at most log V below it, and tiles beyond have their tau), C is
-// not small against Σ|c| and the factor does not underflow; 1 for rows whose dz has to be written
-// out; 0 for rows without a gradient.
-template <bool BWD>
-__global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const HeadRowArgs a) {
-  griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
-  __shared__ int sid[kHeadRowWarps][kHeadMaxIds], ordered[kHeadRowWarps][kHeadMaxIds];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot = blockIdx.x * kHeadRowWarps + w;
-  if (slot >= a.M) return;  // whole warps
-  if (BWD && a.m_dev != nullptr && a.slot_of[slot] < 0) {  // the caller's row of this number was left out
-    uint4* d = reinterpret_cast<uint4*>(a.dX + static_cast<size_t>(slot) * a.D);
-    for (int i = lane; i < a.D / 8; i += 32) d[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  if (a.m_dev != nullptr && slot >= *a.m_dev) return;
-  const int row = a.m_dev != nullptr ? a.rowmap[slot] : slot;
+// The factor f: with g_H = 0 the row's dz is -scale·C·e^{-lse} (C = Σc) times the saved e^z, but for
+// its given tokens: that factor, if lse is within what e^z can hold in bf16 ([-20, 60]: the maximum
+// is at most log V below it, and tiles beyond have their tau), C is not small against Σ|c| and the
+// factor does not underflow; 1 for rows whose dz has to be written out; 0 for rows without a
+// gradient.
+template <bool BWD, typename At>
+__device__ __forceinline__ HeadRowGrad head_row_tokens(const HeadRowArgs& a, int row, int lane, int* sid, At at) {
   const int32_t* ids = a.ids + static_cast<size_t>(row) * a.n;
+  HeadRowGrad g{make_float4(0.f, 0.f, 0.f, 0.f), 0.0f};
   float coef[kHeadPerLane];
-  float csum = 0.0f;
   if (BWD) {
     if (a.teacher != nullptr) {
       const bool any = teacher_log_softmax(ids, a.teacher + static_cast<size_t>(row) * a.n, a.n, a.ignore, a.scale,
                                            lane, coef);
-      const float g = any ? -a.dloss[row] : 0.0f;
+      const float dl = any ? -a.dloss[row] : 0.0f;
 #pragma unroll
-      for (int u = 0; u < kHeadPerLane; ++u) coef[u] = any ? g * expf(coef[u]) : 0.0f;
+      for (int u = 0; u < kHeadPerLane; ++u) coef[u] = any ? dl * expf(coef[u]) : 0.0f;
     } else {
 #pragma unroll
       for (int u = 0; u < kHeadPerLane; ++u) {
@@ -495,46 +489,58 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const Hea
                                                                        : 0.0f;
       }
     }
+    float csum = 0.0f, cabs = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kHeadPerLane; ++u) csum += coef[u];
-    csum = warp_sum(csum);
-    float cabs = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kHeadPerLane; ++u) cabs += fabsf(coef[u]);
-    cabs = warp_sum(cabs);
-    if (lane == 0) {
-      const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
-      const bool none = gh == 0.0f && cabs == 0.0f;  // no gradient, whatever the logits
-      const float lse = none ? 0.0f : a.lse[row];
-      a.rowp[slot] = make_float4(lse * kLog2e, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh * kLn2,
-                                 none ? 0.0f : 1.0f);
-      if (a.rowf != nullptr) {
-        float f = -a.scale * csum * expf(-lse);
-        if (!(gh == 0.0f && lse >= -20.0f && lse <= 60.0f && fabsf(csum) >= cabs * 0x1p-6f && fabsf(f) > 1e-30f)) f = 1.0f;
-        if (none) f = 0.0f;
-        a.rowf[slot] = f;
-      }
+    for (int u = 0; u < kHeadPerLane; ++u) {
+      csum += coef[u];
+      cabs += fabsf(coef[u]);
     }
+    csum = warp_sum(csum);
+    cabs = warp_sum(cabs);
+    const float gh = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+    const bool none = gh == 0.0f && cabs == 0.0f;  // no gradient, whatever the logits
+    const float lse = none ? 0.0f : a.lse[row];
+    g.rp = make_float4(lse * kLog2e, gh != 0.0f ? fmaf(gh, a.ent[row], csum) : csum, gh * kLn2, none ? 0.0f : 1.0f);
+    g.f = -a.scale * csum * expf(-lse);
+    if (!(gh == 0.0f && lse >= -20.0f && lse <= 60.0f && fabsf(csum) >= cabs * 0x1p-6f && fabsf(g.f) > 1e-30f)) g.f = 1.0f;
+    if (none) g.f = 0.0f;
   }
   for (int i = lane; i < a.n; i += 32) {
     const int id = ids[i];
-    sid[w][i] = id == a.ignore || id < 0 || id >= a.V ? 0x7fffffff : id;
+    sid[i] = id == a.ignore || id < 0 || id >= a.V ? 0x7fffffff : id;
   }
   __syncwarp();
 #pragma unroll
   for (int u = 0; u < kHeadPerLane; ++u) {
     const int i = lane + 32 * u;
     if (i < a.n) {
-      const int id = sid[w][i];
+      const int id = sid[i];
       int before = 0;
-      for (int j = 0; j < a.n; ++j) before += sid[w][j] < id || (sid[w][j] == id && j < i);
-      ordered[w][before] = id;
-      a.sorted[static_cast<size_t>(slot) * a.n + before] = make_int2(id, BWD ? __float_as_int(coef[u]) : i);
-      if (BWD && a.sorted_logit != nullptr)
-        a.sorted_logit[static_cast<size_t>(slot) * a.n + before] = a.id_logit[static_cast<size_t>(slot) * a.n + i];
+      for (int j = 0; j < a.n; ++j) before += sid[j] < id || (sid[j] == id && j < i);
+      at(before, id, i, BWD ? coef[u] : 0.0f);
     }
   }
   __syncwarp();
+  return g;
+}
+
+// One warp a row: the row's tokens in order, with their position (forward) or coefficient
+// (backward), and how many precede each tile, for the GEMM epilogues; the forward's bounds
+// cleared, the backward's row coefficients.
+template <bool BWD>
+__global__ void __launch_bounds__(32 * kHeadRowWarps) head_prep_kernel(const HeadRowArgs a) {
+  griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
+  __shared__ int sid[kHeadRowWarps][kHeadMaxIds], ordered[kHeadRowWarps][kHeadMaxIds];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot = blockIdx.x * kHeadRowWarps + w;
+  if (slot >= (a.m_dev != nullptr ? *a.m_dev : a.M)) return;  // whole warps
+  const int row = a.m_dev != nullptr ? a.rowmap[slot] : slot;
+  int2* sorted = a.sorted + static_cast<size_t>(slot) * a.n;
+  const HeadRowGrad g = head_row_tokens<BWD>(a, row, lane, sid[w], [&](int k, int id, int i, float c) {
+    ordered[w][k] = id;
+    sorted[k] = make_int2(id, BWD ? __float_as_int(c) : i);
+  });
+  if (BWD && lane == 0) a.rowp[slot] = g.rp;
   if (a.first != nullptr) {
     const int tiles = (a.V + kHeadTile - 1) / kHeadTile;
     uint8_t* first = a.first + static_cast<size_t>(slot) * tiles;
@@ -807,22 +813,46 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
 }
 
 // The backward from a saved forward prepares the operand of the dX GEMM in place, one block a
-// row; the GEMM multiplies row m of its result by rowf[m] (head_prep_kernel).
+// row; the GEMM multiplies row m of its result by rowf[m] (HeadRowGrad::f).
 //   rowf = -scale·C·e^{-lse}: the saved e^z stand, but for tiles that kept 2^{y-tau} (rare: times
 //     2^tau) and the given tokens, which become dz/rowf from their fp32 logits.
 //   rowf = 1 (an entropy gradient, C small against Σ|c|, an lse that e^z cannot hold): the whole
 //     row becomes dz = scale·(Σ c - p·(Σc + g_H·(log p + H))); bound by HBM, 4·V bytes a row.
 //   rowf = 0: nothing, the GEMM's row is 0.
+// Blocks also clear dX of rows that were left out.
 constexpr int kSavedThreads = 256;
-__global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const HeadArgs h, int V, int np) {
+__global__ void __launch_bounds__(kSavedThreads)
+    head_saved_rows_kernel(const HeadRowArgs a, __nv_bfloat16* expz, const float* taus, int np) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
-  const int row = blockIdx.x, tid = threadIdx.x;
-  if (h.m_dev != nullptr && row >= *h.m_dev) return;
-  const float f = h.rowf[row];
+  __shared__ int sid[kHeadMaxIds], s_id[kHeadMaxIds];
+  __shared__ float s_c[kHeadMaxIds], s_z[kHeadMaxIds];
+  __shared__ HeadRowGrad s_g;
+  const int slot = blockIdx.x, tid = threadIdx.x;
+  if (a.m_dev != nullptr && a.slot_of[slot] < 0) {  // the caller's row of this number was left out
+    uint4* d = reinterpret_cast<uint4*>(a.dX + static_cast<size_t>(slot) * a.D);
+    for (int i = tid; i < a.D / 8; i += kSavedThreads) d[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (a.m_dev != nullptr && slot >= *a.m_dev) return;
+  if (tid < 32) {
+    const int row = a.m_dev != nullptr ? a.rowmap[slot] : slot;
+    const float* z = a.id_logit + static_cast<size_t>(slot) * a.n;
+    const HeadRowGrad g = head_row_tokens<true>(a, row, tid, sid, [&](int k, int id, int i, float c) {
+      s_id[k] = id;
+      s_c[k] = c;
+      s_z[k] = z[i];
+    });
+    if (tid == 0) {
+      s_g = g;
+      a.rowf[slot] = g.f;
+    }
+  }
+  __syncthreads();
+  const float f = s_g.f;
   if (f == 0.0f) return;
-  const float4 rp = h.rowp[row];
-  __nv_bfloat16* zrow = h.expz + static_cast<size_t>(row) * V;
-  const float* tau = h.tau + static_cast<size_t>(row) * np;
+  const float4 rp = s_g.rp;
+  __nv_bfloat16* zrow = expz + static_cast<size_t>(slot) * a.V;
+  const float* tau = taus + static_cast<size_t>(slot) * np;
+  const int V = a.V;
   const bool whole = f == 1.0f;
   if (whole) {
     constexpr int U = 4;
@@ -849,7 +879,7 @@ __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const He
           const float ez = __uint_as_float((j & 1) ? (in[j >> 1] & 0xffff0000u) : (in[j >> 1] << 16));
           float wgt = rp.y;
           if (rp.z != 0.0f && ez > 0.0f) wgt = fmaf(rp.z, lg2_approx(ez) + shift[u], wgt);
-          d[j] = -h.scale * ez * es * wgt;
+          d[j] = -a.scale * ez * es * wgt;
         }
         *reinterpret_cast<uint4*>(zrow + col) = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]),
                                                            pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7]));
@@ -864,16 +894,15 @@ __global__ void __launch_bounds__(kSavedThreads) head_saved_rows_kernel(const He
         zrow[col] = __float2bfloat16_rn(__bfloat162float(zrow[col]) * es);
     }
   }
-  if (h.n == 0) return;
+  if (a.n == 0) return;
   __syncthreads();
-  if (tid < h.n) {
-    const int2* so = h.sorted + static_cast<size_t>(row) * h.n;
-    const int id = so[tid].x;
-    if (id == 0x7fffffff || (tid > 0 && so[tid - 1].x == id)) return;
+  if (tid < a.n) {
+    const int id = s_id[tid];
+    if (id == 0x7fffffff || (tid > 0 && s_id[tid - 1] == id)) return;
     float c = 0.0f;
-    for (int i = tid; i < h.n && so[i].x == id; ++i) c += __int_as_float(so[i].y);
-    const float lp = fmaf(h.id_logit[static_cast<size_t>(row) * h.n + tid], h.c2, -rp.x);
-    const float dz = h.scale * (c - exp2f(lp) * (rp.z != 0.0f ? fmaf(rp.z, lp, rp.y) : rp.y));
+    for (int i = tid; i < a.n && s_id[i] == id; ++i) c += s_c[i];
+    const float lp = fmaf(s_z[tid], a.c2, -rp.x);
+    const float dz = a.scale * (c - exp2f(lp) * (rp.z != 0.0f ? fmaf(rp.z, lp, rp.y) : rp.y));
     zrow[id] = __float2bfloat16_rn(whole ? dz : dz / f);
   }
 }

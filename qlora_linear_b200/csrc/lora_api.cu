@@ -1276,18 +1276,17 @@ size_t head_dx_slot_bytes(long long M, long long D, long long V) {
   return static_cast<size_t>(head_dx_units(M, D, V)) * 262144;
 }
 
-// Backward scratch: sorted (id, coefficient) pairs with their logits, the tiles' first of them, and
-// the coefficients of all rows; then either the pieces of a dX GEMM over the whole vocabulary with,
+// Backward scratch: sorted (id, coefficient) pairs, the tiles' first of them, and the coefficients of
+// all rows; then either the pieces of a dX GEMM over the whole vocabulary with,
 // unless the logits were saved, dz [M, V] behind them, or the fp32 sum of dX with a slice of dz.
 struct HeadBwdLayout {
-  size_t sorted_off = 0, logit_off = 0, first_off = 0, rowp_off = 0, rowf_off = 0;
+  size_t sorted_off = 0, first_off = 0, rowp_off = 0, rowf_off = 0;
   size_t slot_off = 0, whole_dz_off = 0, acc_off = 0, slice_dz_off = 0;
 };
 HeadBwdLayout head_bwd_layout(long long M, long long D, long long V, int n) {
   HeadBwdLayout l;
   l.sorted_off = kStatusBytes;
-  l.logit_off = l.sorted_off + align256(static_cast<size_t>(M) * n * 8);
-  l.first_off = l.logit_off + align256(static_cast<size_t>(M) * n * 4);
+  l.first_off = l.sorted_off + align256(static_cast<size_t>(M) * n * 8);
   l.rowp_off = l.first_off + (n > 0 ? align256(static_cast<size_t>(M) * cdiv(V, kHeadTile)) : 0);
   l.rowf_off = l.rowp_off + align256(static_cast<size_t>(M) * 16);
   l.slot_off = l.rowf_off + align256(static_cast<size_t>(M) * 4);
@@ -1478,24 +1477,26 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
   r.sorted = reinterpret_cast<int2*>(ws + l.sorted_off);
   r.rowp = reinterpret_cast<float4*>(ws + l.rowp_off);
   uint8_t* sv = static_cast<uint8_t*>(saved);
+  r.c2 = static_cast<float>(static_cast<double>(r.scale) * 1.4426950408889634);
   if (saved) {
     r.id_logit = reinterpret_cast<const float*>(sv + head_saved_logit_off(M, V));
-    r.sorted_logit = reinterpret_cast<float*>(ws + l.logit_off);
     r.rowf = reinterpret_cast<float*>(ws + l.rowf_off);
     if (r.teacher && head_fwd_layout(M, D, V, n, 0, true).compact) {
       head_set_map(r, sv + head_saved_map_off(M, V, n), M);
       r.dX = static_cast<__nv_bfloat16*>(dX);
       r.D = static_cast<int>(D);
     }
-  } else if (n > 0) {
-    r.first = ws + l.first_off;
+    launch_k(head_saved_rows_kernel, dim3(static_cast<unsigned>(M)), dim3(kSavedThreads), 0, st, r,
+             static_cast<__nv_bfloat16*>(saved), reinterpret_cast<const float*>(sv + head_tau_off(M, V)), tiles);
+  } else {
+    if (n > 0) r.first = ws + l.first_off;
+    launch_k(head_prep_kernel<true>, dim3(cdiv(M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
   }
-  launch_k(head_prep_kernel<true>, dim3(cdiv(M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
   count_launch();
   TRY(last_launch());
   HeadArgs h{};
   h.scale = r.scale;
-  h.c2 = r.c2 = static_cast<float>(static_cast<double>(r.scale) * 1.4426950408889634);
+  h.c2 = r.c2;
   h.n = n;
   h.sorted = r.sorted;
   h.rowp = r.rowp;
@@ -1514,15 +1515,7 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
     lora_weight_t Wc = *W;  // rows [v0, v0 + w) of the head
     Wc.N = w;
     Wc.data = static_cast<const uint8_t*>(W->data) + static_cast<size_t>(v0) * D * 2;
-    if (saved) {
-      h.expz = dz;
-      h.tau = reinterpret_cast<float*>(sv + head_tau_off(M, V));
-      h.id_logit = r.sorted_logit;
-      launch_k(head_saved_rows_kernel, dim3(static_cast<unsigned>(M)), dim3(kSavedThreads), 0, st, h,
-               static_cast<int>(V), tiles);
-      count_launch();
-      TRY(last_launch());
-    } else {
+    if (!saved) {
       PairParams p = ce_params(M, w, D, dz, status, &Wc);
       p.v0 = static_cast<int>(v0);
       p.head = h;
