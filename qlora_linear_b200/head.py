@@ -5,12 +5,25 @@ from __future__ import annotations
 
 import dataclasses
 import threading
+from ctypes import byref
 
 import torch
 
 from . import binding as _b
 
-_current_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() takes 7 us
+# The layers call the library without the binding's wrappers and torch.cuda.current_stream():
+# a call on a small head takes the GPU about as long as these take the host.
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_lib = _b.lib()
+
+
+def _check(status: int, where: str):
+    if status != _b.LORA_OK:
+        raise _b.LoraError(status, where)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 @dataclasses.dataclass
@@ -195,8 +208,10 @@ class LoraTokenLogProbs(_HeadLayer):
                 torch.empty((M, k), dtype=f32, device=dev) if k else None,
                 self._saved(M, n, dev) if save else None, n)
             ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, k), dev, handle)
-            _b.lora_logprob_fwd(X, M, self.W, ids, n, self.ignore_index, self.scale, k, out.logprob, out.entropy,
-                                out.lse, out.top_ids, out.top_logprob, out.saved, ws, stream=handle)
+            _check(_lib.lora_logprob_fwd(X.data_ptr(), M, byref(self.W.c_struct()), _ptr(ids), n, self.ignore_index,
+                                         self.scale, k, _ptr(out.logprob), _ptr(out.entropy), out.lse.data_ptr(),
+                                         _ptr(out.top_ids), _ptr(out.top_logprob), _ptr(out.saved), ws.data_ptr(),
+                                         ws.numel(), handle), "lora_logprob_fwd")
             return out
 
         return self._run(call, X, stream, ids)
@@ -220,8 +235,10 @@ class LoraTokenLogProbs(_HeadLayer):
             out = self._dX(dX, X)
             saved = self._take_saved(fwd, M, n)
             ws = self._bwd_workspace(M, n, saved, dev, handle)
-            _b.lora_logprob_bwd(X, M, self.W, ids, n, self.ignore_index, self.scale, fwd.lse, fwd.entropy, dlogprob,
-                                dentropy, saved, out, ws, stream=handle)
+            _check(_lib.lora_logprob_bwd(X.data_ptr(), M, byref(self.W.c_struct()), _ptr(ids), n, self.ignore_index,
+                                         self.scale, fwd.lse.data_ptr(), _ptr(fwd.entropy), _ptr(dlogprob),
+                                         _ptr(dentropy), _ptr(saved), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                         handle), "lora_logprob_bwd")
             return out
 
         return self._run(call, X, stream, ids, dlogprob, dentropy, fwd.lse, fwd.entropy, fwd.saved)
@@ -253,8 +270,10 @@ class LoraDistill(_HeadLayer):
             out = DistillLoss(torch.empty(M, dtype=torch.float32, device=dev),
                               torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, n, dev) if save else None, n)
             ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, 0), dev, handle)
-            _b.lora_distill_fwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, out.loss, out.lse,
-                                out.saved, ws, stream=handle)
+            _check(_lib.lora_distill_fwd(X.data_ptr(), M, byref(self.W.c_struct()), ids.data_ptr(),
+                                         teacher_logits.data_ptr(), n, self.ignore_index, self.scale,
+                                         out.loss.data_ptr(), out.lse.data_ptr(), _ptr(out.saved), ws.data_ptr(),
+                                         ws.numel(), handle), "lora_distill_fwd")
             return out
 
         return self._run(call, X, stream, ids, teacher_logits)
@@ -270,8 +289,10 @@ class LoraDistill(_HeadLayer):
             out = self._dX(dX, X)
             saved = self._take_saved(fwd, M, n)
             ws = self._bwd_workspace(M, n, saved, dev, handle)
-            _b.lora_distill_bwd(X, M, self.W, ids, teacher_logits, n, self.ignore_index, self.scale, fwd.lse, dloss,
-                                saved, out, ws, stream=handle)
+            _check(_lib.lora_distill_bwd(X.data_ptr(), M, byref(self.W.c_struct()), ids.data_ptr(),
+                                         teacher_logits.data_ptr(), n, self.ignore_index, self.scale,
+                                         fwd.lse.data_ptr(), dloss.data_ptr(), _ptr(saved), out.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), handle), "lora_distill_bwd")
             return out
 
         return self._run(call, X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved)
