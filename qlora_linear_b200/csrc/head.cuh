@@ -812,49 +812,52 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   }
 }
 
-// The backward from a saved forward prepares the operand of the dX GEMM in place, one block a
-// row; the GEMM multiplies row m of its result by rowf[m] (HeadRowGrad::f).
+// The backward from a saved forward prepares the operand of the dX GEMM in place; the GEMM
+// multiplies row m of its result by rowf[m] (HeadRowGrad::f).
 //   rowf = -scale·C·e^{-lse}: the saved e^z stand, but for tiles that kept 2^{y-tau} (rare: times
 //     2^tau) and the given tokens, which become dz/rowf from their fp32 logits.
 //   rowf = 1 (an entropy gradient, C small against Σ|c|, an lse that e^z cannot hold): the whole
 //     row becomes dz = scale·(Σ c - p·(Σc + g_H·(log p + H))); bound by HBM, 4·V bytes a row.
 //   rowf = 0: nothing, the GEMM's row is 0.
-// Blocks also clear dX of rows that were left out.
-constexpr int kSavedThreads = 256;
+// A block takes `per` <= 8 rows, a warp each for their tokens, and writes out its whole rows one
+// after the other; more rows a block where there are blocks enough (per = 1 for 13653 rows x 408
+// took 71 us, bound by the blocks' latency).  Blocks also clear dX of rows that were left out.
+constexpr int kSavedThreads = 256, kSavedRows = kSavedThreads / 32;
 __global__ void __launch_bounds__(kSavedThreads)
-    head_saved_rows_kernel(const HeadRowArgs a, __nv_bfloat16* expz, const float* taus, int np) {
+    head_saved_rows_kernel(const HeadRowArgs a, __nv_bfloat16* expz, const float* taus, int np, int per) {
   griddep_enter();  // the previous kernel in the stream completed (see ptx.cuh)
-  __shared__ int sid[kHeadMaxIds], s_id[kHeadMaxIds];
-  __shared__ float s_c[kHeadMaxIds], s_z[kHeadMaxIds];
-  __shared__ HeadRowGrad s_g;
-  const int slot = blockIdx.x, tid = threadIdx.x;
-  if (a.m_dev != nullptr && a.slot_of[slot] < 0) {  // the caller's row of this number was left out
-    uint4* d = reinterpret_cast<uint4*>(a.dX + static_cast<size_t>(slot) * a.D);
-    for (int i = tid; i < a.D / 8; i += kSavedThreads) d[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  if (a.m_dev != nullptr && slot >= *a.m_dev) return;
-  if (tid < 32) {
-    const int row = a.m_dev != nullptr ? a.rowmap[slot] : slot;
-    const float* z = a.id_logit + static_cast<size_t>(slot) * a.n;
-    const HeadRowGrad g = head_row_tokens<true>(a, row, tid, sid, [&](int k, int id, int i, float c) {
-      s_id[k] = id;
-      s_c[k] = c;
-      s_z[k] = z[i];
-    });
-    if (tid == 0) {
-      s_g = g;
-      a.rowf[slot] = g.f;
+  __shared__ int sid[kSavedRows][kHeadMaxIds], s_id[kSavedRows][kHeadMaxIds];
+  __shared__ float s_c[kSavedRows][kHeadMaxIds], s_z[kSavedRows][kHeadMaxIds];
+  __shared__ HeadRowGrad s_g[kSavedRows];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  const int slot0 = blockIdx.x * per, V = a.V;
+  const int rows = a.m_dev != nullptr ? *a.m_dev : a.M;
+  if (w < per && slot0 + w < a.M) {
+    const int slot = slot0 + w;
+    if (a.m_dev != nullptr && a.slot_of[slot] < 0) {  // the caller's row of this number was left out
+      uint4* d = reinterpret_cast<uint4*>(a.dX + static_cast<size_t>(slot) * a.D);
+      for (int i = lane; i < a.D / 8; i += 32) d[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (slot < rows) {
+      const float* z = a.id_logit + static_cast<size_t>(slot) * a.n;
+      const HeadRowGrad g = head_row_tokens<true>(a, a.m_dev != nullptr ? a.rowmap[slot] : slot, lane, sid[w],
+                                                  [&](int k, int id, int i, float c) {
+                                                    s_id[w][k] = id;
+                                                    s_c[w][k] = c;
+                                                    s_z[w][k] = z[i];
+                                                  });
+      if (lane == 0) {
+        s_g[w] = g;
+        a.rowf[slot] = g.f;
+      }
     }
   }
   __syncthreads();
-  const float f = s_g.f;
-  if (f == 0.0f) return;
-  const float4 rp = s_g.rp;
-  __nv_bfloat16* zrow = expz + static_cast<size_t>(slot) * a.V;
-  const float* tau = taus + static_cast<size_t>(slot) * np;
-  const int V = a.V;
-  const bool whole = f == 1.0f;
-  if (whole) {
+  for (int r = 0; r < per && slot0 + r < rows; ++r) {
+    if (s_g[r].f != 1.0f) continue;  // the same for all threads
+    const float4 rp = s_g[r].rp;
+    __nv_bfloat16* zrow = expz + static_cast<size_t>(slot0 + r) * V;
+    const float* tau = taus + static_cast<size_t>(slot0 + r) * np;
     constexpr int U = 4;
     for (int c0 = tid * 8; c0 < V; c0 += kSavedThreads * 8 * U) {
       uint4 x[U];
@@ -885,25 +888,32 @@ __global__ void __launch_bounds__(kSavedThreads)
                                                            pack_bf16x2(d[4], d[5]), pack_bf16x2(d[6], d[7]));
       }
     }
-  } else {
-    for (int t = tid; t < np; t += kSavedThreads) {
+  }
+  __syncthreads();
+  if (w >= per || slot0 + w >= rows || s_g[w].f == 0.0f) return;  // whole warps
+  const float f = s_g[w].f;
+  const float4 rp = s_g[w].rp;
+  __nv_bfloat16* zrow = expz + static_cast<size_t>(slot0 + w) * V;
+  if (f != 1.0f) {
+    const float* tau = taus + static_cast<size_t>(slot0 + w) * np;
+#pragma unroll 4
+    for (int t = lane; t < np; t += 32) {
       const float tt = tau[t];
       if (tt == 0.0f) continue;
       const float es = exp2f(tt);  // at most 2^86.6, an lse of 60
       for (int col = t * kHeadTile; col < min(V, (t + 1) * kHeadTile); ++col)
         zrow[col] = __float2bfloat16_rn(__bfloat162float(zrow[col]) * es);
     }
+    __syncwarp();
   }
-  if (a.n == 0) return;
-  __syncthreads();
-  if (tid < a.n) {
-    const int id = s_id[tid];
-    if (id == 0x7fffffff || (tid > 0 && s_id[tid - 1] == id)) return;
+  for (int i = lane; i < a.n; i += 32) {
+    const int id = s_id[w][i];
+    if (id == 0x7fffffff || (i > 0 && s_id[w][i - 1] == id)) continue;
     float c = 0.0f;
-    for (int i = tid; i < a.n && s_id[i] == id; ++i) c += s_c[i];
-    const float lp = fmaf(s_z[tid], a.c2, -rp.x);
+    for (int j = i; j < a.n && s_id[w][j] == id; ++j) c += s_c[w][j];
+    const float lp = fmaf(s_z[w][i], a.c2, -rp.x);
     const float dz = a.scale * (c - exp2f(lp) * (rp.z != 0.0f ? fmaf(rp.z, lp, rp.y) : rp.y));
-    zrow[id] = __float2bfloat16_rn(whole ? dz : dz / f);
+    zrow[id] = __float2bfloat16_rn(f == 1.0f ? dz : dz / f);
   }
 }
 

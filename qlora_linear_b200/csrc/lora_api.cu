@@ -1486,8 +1486,10 @@ lora_status_t head_bwd_core(const void* X, long long M, const lora_weight_t* W, 
       r.dX = static_cast<__nv_bfloat16*>(dX);
       r.D = static_cast<int>(D);
     }
-    launch_k(head_saved_rows_kernel, dim3(static_cast<unsigned>(M)), dim3(kSavedThreads), 0, st, r,
-             static_cast<__nv_bfloat16*>(saved), reinterpret_cast<const float*>(sv + head_tau_off(M, V)), tiles);
+    int per = 1;  // rows a block: at least four blocks an SM
+    while (per < kSavedRows && M >= 2LL * per * 4 * 148) per *= 2;
+    launch_k(head_saved_rows_kernel, dim3(cdiv(M, per)), dim3(kSavedThreads), 0, st, r,
+             static_cast<__nv_bfloat16*>(saved), reinterpret_cast<const float*>(sv + head_tau_off(M, V)), tiles, per);
   } else {
     if (n > 0) r.first = ws + l.first_off;
     launch_k(head_prep_kernel<true>, dim3(cdiv(M, kHeadRowWarps)), dim3(32 * kHeadRowWarps), 0, st, r);
