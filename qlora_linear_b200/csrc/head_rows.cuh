@@ -11,7 +11,9 @@
 // W goes through a ring of stages of 128 entries × 128 of the D columns, which HBM serves in
 // 256-byte pieces, each CTA starting at another column (V = 128256, D = 4096, 1 row: 182 us;
 // 186 us with 256 entries × 64, 196 us with 64 × 256).  A range's last tile takes boxes of 64, 32
-// and 16 entries.
+// and 16 entries.  The producer and the MMA issuer run as whole warps that issue under elect_one():
+// under `lane == 0` a TMA load cost its thread 230 cycles and an MMA 78, 1200 and 900 a fill, which
+// bounded short ranges (16 rows, V = 280, D = 8192: 48 us, now 29) and left HBM little slack.
 //
 // Epilogue: a lane holds one entry's logits of 32 rows.  Sums over the 32 entries of a warp go
 // by transposing reductions (31 shuffles for 32 rows, lane i ending with row i), so a warp keeps the
@@ -31,7 +33,9 @@ constexpr int HR_BN = 128;          // vocabulary entries a tile
 constexpr int HR_BK = 128;          // of D per stage: two 64-wide swizzle atoms
 constexpr int HR_ATOMS = HR_BK / 64;
 constexpr int HR_UNIT = 16;         // granularity of the CTAs' ranges
-constexpr int HR_MAX_STAGES = 6;
+// 128 KB of W in flight a SM; with more HBM gets slower (V = 128256, D = 4096, 5 rows: 165, 160, 163
+// and 167 us with 3, 4, 5 and 6 stages).
+constexpr int HR_MAX_STAGES = 4;
 constexpr int HR_THREADS = 192;
 constexpr int HR_WARPS = 4;         // epilogue warps: partials a CTA
 constexpr int HR_W_BYTES = HR_BN * HR_BK * 2;  // 32 KB
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    {
       int stage = 0;
       uint32_t phase = 0;
       long long fills = 0;
@@ -144,23 +148,26 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
           break;
         }
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
+          if (!mbar_wait_warp(smem_u32(&empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
           const int kx = kb + shift < nkb ? kb + shift : kb + shift - nkb;
           const uint32_t sW = smem_u32(smem + stage * stage_bytes);
           const uint32_t bar = smem_u32(&full[stage]);
-          mbar_arrive_expect_tx(bar, rows * HR_BK * 2 + xbytes);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, rows * HR_BK * 2 + xbytes);
 #pragma unroll
-          for (int a = 0; a < HR_ATOMS; ++a) {
-            const int x = kx * HR_BK + a * 64;
-            int u = 0;
+            for (int a = 0; a < HR_ATOMS; ++a) {
+              const int x = kx * HR_BK + a * 64;
+              int u = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (rows & (HR_BN >> i)) {
-                tma_load_2d(sW + a * (HR_W_BYTES / HR_ATOMS) + u * 128, &tmW.box[i], bar, x, v0 + u);
-                u += HR_BN >> i;
-              }
-            tma_load_2d(sW + HR_W_BYTES + a * (xbytes / HR_ATOMS), &tmX, bar, x, 0);
+              for (int i = 0; i < 4; ++i)
+                if (rows & (HR_BN >> i)) {
+                  tma_load_2d(sW + a * (HR_W_BYTES / HR_ATOMS) + u * 128, &tmW.box[i], bar, x, v0 + u);
+                  u += HR_BN >> i;
+                }
+              tma_load_2d(sW + HR_W_BYTES + a * (xbytes / HR_ATOMS), &tmX, bar, x, 0);
+            }
           }
+          __syncwarp();
           ++fills;
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
@@ -169,42 +176,50 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
       if (!ok) {
         const WaitCtl drain_wc{&never_s, nullptr, p.wait_ns};
         for (long long f = fills > S ? fills - S : 0; f < fills; ++f)
-          mbar_wait(smem_u32(&full[f % S]), static_cast<uint32_t>((f / S) & 1), drain_wc);
+          mbar_wait_warp(smem_u32(&full[f % S]), static_cast<uint32_t>((f / S) & 1), drain_wc);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    {
       // entries a last tile did not load hold what shared memory held: their lanes are not used
       const uint32_t idesc = idesc_bf16_f32(HR_BN, hr_n(p.M), false, false);
+      const uint64_t w_desc = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t x_desc = sdesc_sw128(smem_u32(smem) + HR_W_BYTES, 16, 1024);
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       int acc = 0;
       bool ok = true;
       for (int t = 0; ok && t < ntiles; ++t) {
-        if (!mbar_wait(smem_u32(&tempty[acc]), acc_phase ^ 1u, wc)) break;
+        if (!mbar_wait_warp(smem_u32(&tempty[acc]), acc_phase ^ 1u, wc)) break;
         tc_fence_after();
+        const uint64_t w_atom = (HR_W_BYTES / HR_ATOMS) >> 4, x_atom = (xbytes / HR_ATOMS) >> 4;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(smem_u32(&full[stage]), phase, wc)) { ok = false; break; }
+          if (!mbar_wait_warp(smem_u32(&full[stage]), phase, wc)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sW = smem_u32(smem + stage * stage_bytes);
+          // the descriptors' address field counts 16 bytes: a step of 16 columns is 2
+          const uint64_t wd = w_desc + ((stage * stage_bytes) >> 4), xd = x_desc + ((stage * stage_bytes) >> 4);
+          const uint32_t d = tmem_base + acc * HR_ROWS;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < HR_BK / 16; ++k)
-            tc_mma_bf16(tmem_base + acc * HR_ROWS,
-                        sdesc_sw128(sW + (k >> 2) * (HR_W_BYTES / HR_ATOMS) + (k & 3) * 32, 16, 1024),
-                        sdesc_sw128(sW + HR_W_BYTES + (k >> 2) * (xbytes / HR_ATOMS) + (k & 3) * 32, 16, 1024), idesc,
-                        (kb > 0 || k > 0) ? 1u : 0u);
-          tc_commit(smem_u32(&empty[stage]));
+            for (int k = 0; k < HR_BK / 16; ++k)
+              tc_mma_bf16(d, wd + (k >> 2) * w_atom + (k & 3) * 2, xd + (k >> 2) * x_atom + (k & 3) * 2, idesc,
+                          (kb > 0 || k > 0) ? 1u : 0u);
+            tc_commit(smem_u32(&empty[stage]));
+          }
+          __syncwarp();
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        tc_commit(smem_u32(&tfull[acc]));
+        if (elect_one()) tc_commit(smem_u32(&tfull[acc]));
+        __syncwarp();
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       // every MMA issued so far must finish before TMEM is released
-      tc_commit(smem_u32(&drain));
+      if (elect_one()) tc_commit(smem_u32(&drain));
+      __syncwarp();
       const WaitCtl drain_wc{&never_s, nullptr, p.wait_ns};
-      mbar_wait(smem_u32(&drain), 0, drain_wc);
+      mbar_wait_warp(smem_u32(&drain), 0, drain_wc);
     }
   } else {
     // ------------------------------------------------------------ epilogue
