@@ -29,7 +29,9 @@
 // that streamk_fixup_kernel adds up.
 //
 // Roles per CTA: warp 0 TMA producer, warp 1 MMA issuer (leader) and TMEM owner,
-// warps 2-5 epilogue.
+// warps 2-5 epilogue.  The first two run as whole warps and issue under elect_one(): under
+// `lane == 0` the four TMA loads of a fill took their thread about as long as its MMAs take
+// (777 rows x 32000 x 2048: 140 us, now 135).
 #pragma once
 
 #include "gemm_common.cuh"
@@ -145,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    {
       int stage = 0;
       uint32_t phase = 0;
       long long fills = 0;
@@ -164,47 +166,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
           break;
         }
         for (int kb = un.f0; kb < un.f1; ++kb) {
-          if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
+          if (!mbar_wait_warp(smem_u32(&empty[stage]), phase ^ 1u, wc)) { ok = false; break; }
           const bool ext = kb >= nkb;
           if (!lora_check(ext ? kb - nkb < n_ext : kb * C::BK < p.Kred, wc)) { ok = false; break; }
           const uint32_t sA = smem_u32(smem + stage * C::STAGE_BYTES);
           const uint32_t sB = sA + C::A_BYTES;
           const uint32_t full_l = mapa_shared(smem_u32(&full[stage]), 0);
-          if (leader) {
-            uint32_t per_cta;
-            if (!ext) per_cta = C::A_BYTES + C::B_BYTES;
-            else per_cta = ext_atoms * (C::A_BYTES / 2) + (B_MN ? C::B_BYTES : ext_atoms * (C::B_BYTES / 2));
-            mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * per_cta);
-          }
-          // every box is 64 wide × 128 rows; a K-major operand takes one box per
-          // 64-wide K atom, an MN-major one (backward weight) one box per 64-wide MN chunk
-          if (!ext) {
-            tma_load_2d_pair(sA, &tmA, full_l, kb * C::BK, arow);
-            tma_load_2d_pair(sA + C::A_BYTES / 2, &tmA, full_l, kb * C::BK + C::ATOM, arow);
-            if (!B_MN) {
-              tma_load_2d_pair(sB, &tmB, full_l, kb * C::BK, brow);
-              tma_load_2d_pair(sB + C::B_BYTES / 2, &tmB, full_l, kb * C::BK + C::ATOM, brow);
-            } else {
-              tma_load_2d_pair(sB, &tmB, full_l, brow, kb * C::BK);
-              tma_load_2d_pair(sB + C::B_BYTES / 2, &tmB, full_l, brow + C::ATOM, kb * C::BK);
+          if (elect_one()) {
+            if (leader) {
+              uint32_t per_cta;
+              if (!ext) per_cta = C::A_BYTES + C::B_BYTES;
+              else per_cta = ext_atoms * (C::A_BYTES / 2) + (B_MN ? C::B_BYTES : ext_atoms * (C::B_BYTES / 2));
+              mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * per_cta);
             }
-          } else {
-            int seg = 0;
-            while (seg + 1 < p.nseg && nb >= p.seg_end_tile[seg]) ++seg;
-            const int e0 = seg * p.e_seg_stride;  // this tile's columns of E
-            for (int h = 0; h < ext_atoms; ++h)
-              tma_load_2d_pair(sA + h * (C::A_BYTES / 2), &tmE, full_l, e0 + h * C::ATOM, arow);
-            if (!B_MN) {
-              // the SwiGLU forward's odd CTA reads F from x = -f_shift: its first f_shift
-              // columns are the zero fill, so the gate half of E meets zeros
-              const int fx = EPI == EPI_SWIGLU_FWD ? -static_cast<int>(rank) * p.f_shift : 0;
+            // every box is 64 wide × 128 rows; a K-major operand takes one box per
+            // 64-wide K atom, an MN-major one (backward weight) one box per 64-wide MN chunk
+            if (!ext) {
+              tma_load_2d_pair(sA, &tmA, full_l, kb * C::BK, arow);
+              tma_load_2d_pair(sA + C::A_BYTES / 2, &tmA, full_l, kb * C::BK + C::ATOM, arow);
+              if (!B_MN) {
+                tma_load_2d_pair(sB, &tmB, full_l, kb * C::BK, brow);
+                tma_load_2d_pair(sB + C::B_BYTES / 2, &tmB, full_l, kb * C::BK + C::ATOM, brow);
+              } else {
+                tma_load_2d_pair(sB, &tmB, full_l, brow, kb * C::BK);
+                tma_load_2d_pair(sB + C::B_BYTES / 2, &tmB, full_l, brow + C::ATOM, kb * C::BK);
+              }
+            } else {
+              int seg = 0;
+              while (seg + 1 < p.nseg && nb >= p.seg_end_tile[seg]) ++seg;
+              const int e0 = seg * p.e_seg_stride;  // this tile's columns of E
               for (int h = 0; h < ext_atoms; ++h)
-                tma_load_2d_pair(sB + h * (C::B_BYTES / 2), &tmF, full_l, fx + h * C::ATOM, brow);
-            } else {
-              tma_load_2d_pair(sB, &tmF, full_l, brow, 0);
-              tma_load_2d_pair(sB + C::B_BYTES / 2, &tmF, full_l, brow + C::ATOM, 0);
+                tma_load_2d_pair(sA + h * (C::A_BYTES / 2), &tmE, full_l, e0 + h * C::ATOM, arow);
+              if (!B_MN) {
+                // the SwiGLU forward's odd CTA reads F from x = -f_shift: its first f_shift
+                // columns are the zero fill, so the gate half of E meets zeros
+                const int fx = EPI == EPI_SWIGLU_FWD ? -static_cast<int>(rank) * p.f_shift : 0;
+                for (int h = 0; h < ext_atoms; ++h)
+                  tma_load_2d_pair(sB + h * (C::B_BYTES / 2), &tmF, full_l, fx + h * C::ATOM, brow);
+              } else {
+                tma_load_2d_pair(sB, &tmF, full_l, brow, 0);
+                tma_load_2d_pair(sB + C::B_BYTES / 2, &tmF, full_l, brow + C::ATOM, 0);
+              }
             }
           }
+          __syncwarp();
           ++fills;
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -216,13 +221,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
         for (long long f = first; f < fills; ++f) {
           const int s = static_cast<int>(f % C::STAGES);
           const uint32_t ph = static_cast<uint32_t>((f / C::STAGES) & 1);
-          if (leader) mbar_wait(smem_u32(&full[s]), ph, drain_wc);
+          if (leader) mbar_wait_warp(smem_u32(&full[s]), ph, drain_wc);
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
-    if (leader && lane == 0) {
+    if (leader) {
       constexpr uint32_t idesc = idesc_bf16_f32(C::BM, C::BN, false, B_MN);
       int stage = 0;
       uint32_t phase = 0;
@@ -232,35 +237,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       UnitWalk w(pair, npairs, ntiles, tile_fills, sk, p.sk_dp_tiles, splits);
       Unit un;
       while (ok && w.next(un)) {
-        if (!mbar_wait<true>(smem_u32(&tempty[acc]), acc_phase ^ 1u, wc)) { ok = false; break; }
+        if (!mbar_wait_warp<true>(smem_u32(&tempty[acc]), acc_phase ^ 1u, wc)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * C::BN);
         for (int kb = un.f0; kb < un.f1; ++kb) {
-          if (!mbar_wait(smem_u32(&full[stage]), phase, wc)) { ok = false; break; }
+          if (!mbar_wait_warp(smem_u32(&full[stage]), phase, wc)) { ok = false; break; }
           tc_fence_after();
           const bool ext = kb >= nkb;
           const uint32_t sA = smem_u32(smem + stage * C::STAGE_BYTES);
           const uint32_t sB = sA + C::A_BYTES;
           const int nk = ext ? (p.r + 15) / 16 : C::BK / 16;
-          for (int k = 0; k < nk; ++k) {
-            // K step k: atom k/4, 32-byte column (k%4) inside the K-major atom; for the
-            // MN-major operand 16 K rows (2 KB) further down its 128-row chunks
-            const uint32_t koff = (k >> 2) * (C::A_BYTES / 2) + (k & 3) * 32;
-            const uint64_t ad = sdesc_sw128(sA + koff, 16, 1024);
-            const uint64_t bd = B_MN ? sdesc_sw128(sB + k * 2048, C::B_BYTES / 2, 1024) : sdesc_sw128(sB + koff, 16, 1024);
-            tc_mma_bf16_pair(d, ad, bd, idesc, (kb > un.f0 || k > 0) ? 1u : 0u);
+          if (elect_one()) {
+            for (int k = 0; k < nk; ++k) {
+              // K step k: atom k/4, 32-byte column (k%4) inside the K-major atom; for the
+              // MN-major operand 16 K rows (2 KB) further down its 128-row chunks
+              const uint32_t koff = (k >> 2) * (C::A_BYTES / 2) + (k & 3) * 32;
+              const uint64_t ad = sdesc_sw128(sA + koff, 16, 1024);
+              const uint64_t bd = B_MN ? sdesc_sw128(sB + k * 2048, C::B_BYTES / 2, 1024) : sdesc_sw128(sB + koff, 16, 1024);
+              tc_mma_bf16_pair(d, ad, bd, idesc, (kb > un.f0 || k > 0) ? 1u : 0u);
+            }
+            tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
           }
-          tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
+          __syncwarp();
           if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        tc_commit_pair_mc(smem_u32(&tfull[acc]), 0x3);
+        if (elect_one()) tc_commit_pair_mc(smem_u32(&tfull[acc]), 0x3);
+        __syncwarp();
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       // every pair MMA issued so far must finish before TMEM is released
-      tc_commit_pair(smem_u32(drain));
+      if (elect_one()) tc_commit_pair(smem_u32(drain));
+      __syncwarp();
       const WaitCtl drain_wc{never_flag, nullptr, p.wait_ns};
-      mbar_wait(smem_u32(drain), 0, drain_wc);
+      mbar_wait_warp(smem_u32(drain), 0, drain_wc);
     }
   } else if (warp < 2 + NEPI) {
     // ------------------------------------------------------------ epilogue (both CTAs)

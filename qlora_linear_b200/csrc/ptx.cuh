@@ -128,12 +128,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
 
 // Whole-warp bounded wait that keeps the warp converged (needed before the
 // .sync.aligned tcgen05 loads): lanes poll together, lane 0 owns the clock.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& w) {
   const uint32_t lane = threadIdx.x & 31u;
   uint64_t t0 = 0;
   if (lane == 0) t0 = global_timer_ns();
   while (true) {
-    const bool ok = mbar_try_wait(bar, parity);
+    const bool ok = mbar_try_wait<CLUSTER>(bar, parity);
     if (__all_sync(0xffffffffu, ok)) return true;
     uint32_t give_up = 0;
     if (lane == 0) {
