@@ -55,6 +55,14 @@ int32_t lora_testing_xpass_tma(int64_t M, int64_t K, int32_t r);
 int32_t lora_testing_dual_blocking(int64_t M, int64_t C, int32_t r, int32_t mode, int32_t* out4);
 
 /*
+ * Pieces into which the LM head's dX GEMM (M rows, width D, vocabulary V) cuts each of its
+ * ceil(M/256)·ceil(D/256) tiles' reduction when `rows` <= M rows have a gradient (rows = M: every
+ * one, or rows that were not compacted); *units (host memory) gets the number of fp32 pieces of
+ * 256 × 256 the workspace holds.  -1 for invalid sizes.  A pure function of its arguments.
+ */
+int32_t lora_testing_head_splits(int64_t M, int64_t D, int64_t V, int64_t rows, int32_t* units);
+
+/*
  * Launches the tensor-core rank-r row projection (X·Aᵀ at rank r, 16 < r <= 128, r % 8 == 0)
  * over P [rows, red] (device bf16, row-major) and A [r, red] (device bf16) with one output
  * tile more than `rows` holds: that tile starts at row 128·ceil(rows/128), past the last

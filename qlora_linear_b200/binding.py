@@ -46,6 +46,7 @@ EXPORTED = (
     "lora_testing_tcproj_extra_tile", "lora_testing_tcproj_splits",
     "lora_head_fwd_workspace_bytes", "lora_head_bwd_workspace_bytes", "lora_head_saved_bytes",
     "lora_logprob_fwd", "lora_logprob_bwd", "lora_distill_fwd", "lora_distill_bwd",
+    "lora_testing_head_splits",
 )
 
 LORA_HEAD_MAX_IDS = 128  # given tokens (or teacher entries) a row
@@ -130,6 +131,8 @@ def _load() -> ctypes.CDLL:
     lib.lora_ce_fwd.restype = i32
     lib.lora_ce_bwd.argtypes = [vp, i64, W, vp, i32, vp, vp, vp, vp, sz, vp]
     lib.lora_ce_bwd.restype = i32
+    lib.lora_testing_head_splits.argtypes = [i64, i64, i64, i64, ctypes.POINTER(i32)]
+    lib.lora_testing_head_splits.restype = i32
     lib.lora_head_fwd_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
     lib.lora_head_fwd_workspace_bytes.restype = sz
     lib.lora_head_bwd_workspace_bytes.argtypes = [i64, i64, i64, i32, i64]
@@ -332,6 +335,13 @@ def lora_testing_dual_blocking(M: int, C: int, r: int, mode: int = 0):
     out = (ctypes.c_int32 * 4)()
     used = int(_lib.lora_testing_dual_blocking(int(M), int(C), int(r), int(mode), out))
     return used, tuple(int(v) for v in out)
+
+
+def lora_testing_head_splits(M: int, D: int, V: int, rows: int) -> tuple[int, int]:
+    """(pieces a tile of the head's dX GEMM, pieces the workspace holds) for ``rows`` rows of M."""
+    units = ctypes.c_int32(0)
+    s = int(_lib.lora_testing_head_splits(int(M), int(D), int(V), int(rows), ctypes.byref(units)))
+    return s, units.value
 
 
 def lora_testing_xpass_tma(M: int, K: int, r: int) -> int:

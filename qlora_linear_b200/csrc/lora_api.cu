@@ -2068,6 +2068,12 @@ int32_t lora_testing_gemm_streamk(int64_t M, int64_t Nout, int64_t Kred, int32_t
   return static_cast<int32_t>(tiles - g.dp_tiles);
 }
 
+int32_t lora_testing_head_splits(int64_t M, int64_t D, int64_t V, int64_t rows, int32_t* units) {
+  if (!head_sizes_ok(M, D, V, 0, 0) || rows < 0 || rows > M || !units) return -1;
+  *units = head_dx_units(M, D, V);
+  return rows == M ? head_dx_splits_of(M, D, V) : head_dx_splits(head_dx_tiles(rows, D), cdiv(V, 128), *units);
+}
+
 int32_t lora_testing_dual_blocking(int64_t M, int64_t C, int32_t r, int32_t mode, int32_t* out4) {
   if (!out4 || M <= 0 || C <= 0 || r < 1 || r > 128 || mode < DP_BOTH || mode > DP_COLS) return -1;
   const DualSplit d = dual_split(M, C, r, mode);
