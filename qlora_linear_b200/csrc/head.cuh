@@ -896,13 +896,19 @@ __global__ void __launch_bounds__(kSavedThreads)
   __nv_bfloat16* zrow = expz + static_cast<size_t>(slot0 + w) * V;
   if (f != 1.0f) {
     const float* tau = taus + static_cast<size_t>(slot0 + w) * np;
-#pragma unroll 4
-    for (int t = lane; t < np; t += 32) {
-      const float tt = tau[t];
-      if (tt == 0.0f) continue;
-      const float es = exp2f(tt);  // at most 2^86.6, an lse of 60
-      for (int col = t * kHeadTile; col < min(V, (t + 1) * kHeadTile); ++col)
-        zrow[col] = __float2bfloat16_rn(__bfloat162float(zrow[col]) * es);
+    constexpr int U = 8;  // loads in flight
+    for (int t0 = lane; t0 < np; t0 += 32 * U) {
+      float tt[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) tt[u] = t0 + 32 * u < np ? tau[t0 + 32 * u] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (tt[u] == 0.0f) continue;
+        const int t = t0 + 32 * u;
+        const float es = exp2f(tt[u]);  // at most 2^86.6, an lse of 60
+        for (int col = t * kHeadTile; col < min(V, (t + 1) * kHeadTile); ++col)
+          zrow[col] = __float2bfloat16_rn(__bfloat162float(zrow[col]) * es);
+      }
     }
     __syncwarp();
   }
