@@ -9,8 +9,8 @@
 // limit lowered the clock and one row took 194 us instead of 171.)
 //
 // W goes through a ring of stages of 128 entries × 128 of the D columns, which HBM serves in
-// 256-byte pieces, each CTA starting at another column (V = 128256, D = 4096, 1 row: 182 us;
-// 186 us with 256 entries × 64, 196 us with 64 × 256).  A range's last tile takes boxes of 64, 32
+// 256-byte pieces, each CTA starting at another column (V = 128256, D = 4096, 1 row, with an earlier
+// issue loop: 182 us; 186 us with 256 entries × 64, 196 us with 64 × 256).  A range's last tile takes boxes of 64, 32
 // and 16 entries.  The producer and the MMA issuer run as whole warps that issue under elect_one():
 // under `lane == 0` a TMA load cost its thread 230 cycles and an MMA 78, 1200 and 900 a fill, which
 // bounded short ranges (16 rows, V = 280, D = 8192: 48 us, now 29) and left HBM little slack.
