@@ -30,7 +30,7 @@ def _ptr(t):
 class TokenLogProbs:
     """What :meth:`LoraTokenLogProbs.forward` returns.  ``logprob`` has the shape of the ids
     given (None without ids); ``entropy`` [M]; ``lse`` [M]; ``top_ids`` int32 and
-    ``top_logprob`` [M, k] (None for k = 0).  ``saved`` and ``tokens`` belong to the backward."""
+    ``top_logprob`` [M, k] (None for k = 0).  The other fields belong to the backward."""
 
     logprob: torch.Tensor | None
     lse: torch.Tensor
@@ -39,17 +39,21 @@ class TokenLogProbs:
     top_logprob: torch.Tensor | None = None
     saved: torch.Tensor | None = None
     tokens: int = 0
+    stream: int = 0         # the stream that saved was taken on
+    captured: bool = False  # the forward ran under graph capture
 
 
 @dataclasses.dataclass
 class DistillLoss:
-    """What :meth:`LoraDistill.forward` returns: ``loss`` [M], ``lse`` [M]; ``saved`` and ``tokens``
-    belong to the backward."""
+    """What :meth:`LoraDistill.forward` returns: ``loss`` [M], ``lse`` [M]; the other fields belong
+    to the backward."""
 
     loss: torch.Tensor
     lse: torch.Tensor
     saved: torch.Tensor | None = None
     tokens: int = 0
+    stream: int = 0         # the stream that saved was taken on
+    captured: bool = False  # the forward ran under graph capture
 
 
 class _HeadLayer:
@@ -58,7 +62,8 @@ class _HeadLayer:
     A call runs on ``stream`` (default: the current stream of X's device) and takes its outputs
     and its workspace from that stream's memory, one workspace a stream, so calls on two streams
     do not meet in it; a lock keeps two threads' calls on one stream apart.  A call under CUDA
-    graph capture takes a workspace of its own from the graph's memory.
+    graph capture takes a workspace of its own from the graph's memory.  Tensors start on a 16-byte
+    boundary (a slice such as ``ids[1:]`` may need a copy).
     """
 
     def __init__(self, W: "_b.LoraWeight", ignore_index: int = -100, temperature: float = 1.0, slice_: int = 0):
@@ -160,12 +165,24 @@ class _HeadLayer:
     def _saved(self, M, n, device):
         return torch.empty(self._bytes(_b.head_saved_bytes, M, self.W.N, n), dtype=torch.uint8, device=device)
 
-    def _take_saved(self, fwd, M, n):
-        """The forward's saved buffer for this backward, which overwrites it (None: recompute)."""
+    def _take_saved(self, fwd, M, n, stream):
+        """The forward's saved buffer for this backward, which overwrites it (None: recompute).  A
+        captured backward runs on every replay, so it leaves the buffer of a forward that does not
+        run with it alone."""
+        if fwd.saved is None or (not fwd.captured and torch.cuda.is_current_stream_capturing()):
+            return None
         saved, fwd.saved = fwd.saved, None
-        if saved is not None and (fwd.tokens != n or saved.numel() != self._bytes(_b.head_saved_bytes, M, self.W.N, n)):
+        if fwd.tokens != n or saved.numel() != self._bytes(_b.head_saved_bytes, M, self.W.N, n):
             raise ValueError("the forward was saved with other sizes (rows, tokens a row or vocabulary)")
+        if fwd.stream != stream:  # not handed out again before this backward has run
+            saved.record_stream(torch.cuda.current_stream())
         return saved
+
+    @staticmethod
+    def _mark(out, stream):
+        if out.saved is not None:
+            out.stream, out.captured = stream, torch.cuda.is_current_stream_capturing()
+        return out
 
     def _bwd_workspace(self, M, n, saved, device, handle):
         slice_ = 0 if saved is not None else self._slice(M)
@@ -185,8 +202,8 @@ class LoraTokenLogProbs(_HeadLayer):
     ``forward(X, ids)``: X bf16 [M, D], ids int32 [M] or [M, n] (n <= 128, entries equal to
     ``ignore_index`` have logprob 0 and no gradient) or None; top_k <= 32.  With ``save=True`` the
     forward keeps 2·M·V bytes for one backward, which then skips recomputing the logits (a later
-    backward of the same forward recomputes them, in vocabulary slices of ``slice_`` rows, by
-    default as many as take 1 GiB).  ``backward`` returns dX for upstream gradients of the
+    backward of the same forward, or one captured into a graph without it, recomputes them, in
+    vocabulary slices of ``slice_`` rows, by default as many as take 1 GiB).  ``backward`` returns dX for upstream gradients of the
     log-probabilities (shape of ids) and of the entropies ([M]).
     """
 
@@ -212,7 +229,7 @@ class LoraTokenLogProbs(_HeadLayer):
                                          self.scale, k, _ptr(out.logprob), _ptr(out.entropy), out.lse.data_ptr(),
                                          _ptr(out.top_ids), _ptr(out.top_logprob), _ptr(out.saved), ws.data_ptr(),
                                          ws.numel(), handle), "lora_logprob_fwd")
-            return out
+            return self._mark(out, handle)
 
         return self._run(call, X, stream, ids)
 
@@ -233,7 +250,7 @@ class LoraTokenLogProbs(_HeadLayer):
 
         def call(handle):
             out = self._dX(dX, X)
-            saved = self._take_saved(fwd, M, n)
+            saved = self._take_saved(fwd, M, n, handle)
             ws = self._bwd_workspace(M, n, saved, dev, handle)
             _check(_lib.lora_logprob_bwd(X.data_ptr(), M, byref(self.W.c_struct()), _ptr(ids), n, self.ignore_index,
                                          self.scale, fwd.lse.data_ptr(), _ptr(fwd.entropy), _ptr(dlogprob),
@@ -274,7 +291,7 @@ class LoraDistill(_HeadLayer):
                                          teacher_logits.data_ptr(), n, self.ignore_index, self.scale,
                                          out.loss.data_ptr(), out.lse.data_ptr(), _ptr(out.saved), ws.data_ptr(),
                                          ws.numel(), handle), "lora_distill_fwd")
-            return out
+            return self._mark(out, handle)
 
         return self._run(call, X, stream, ids, teacher_logits)
 
@@ -287,7 +304,7 @@ class LoraDistill(_HeadLayer):
 
         def call(handle):
             out = self._dX(dX, X)
-            saved = self._take_saved(fwd, M, n)
+            saved = self._take_saved(fwd, M, n, handle)
             ws = self._bwd_workspace(M, n, saved, dev, handle)
             _check(_lib.lora_distill_bwd(X.data_ptr(), M, byref(self.W.c_struct()), ids.data_ptr(),
                                          teacher_logits.data_ptr(), n, self.ignore_index, self.scale,

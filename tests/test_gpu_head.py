@@ -447,6 +447,61 @@ def test_graphs_and_streams(lib):
     del graphs
 
 
+@pytest.mark.parametrize("op", ["logprob", "distill"])
+def test_captured_backward_of_an_ordinary_forward(lib, op):
+    """Replays of a backward captured on its own all give the gradient, and the saved forward still
+    serves an ordinary backward."""
+    inp = make_head_case(HeadCase("graph_bwd", 300, 128, 3000, 4, 143))
+    x = dev_bf16(inp["X"])
+    ids, t, dl, dlp, dent = up(inp, "ids", "teacher", "dloss", "dlogprob", "dentropy")
+    layer = head(lib, inp, lib.LoraTokenLogProbs if op == "logprob" else lib.LoraDistill)
+
+    def fwd(save):
+        return layer.forward(x, ids, save=save) if op == "logprob" else layer.forward(x, ids, t, save=save)
+
+    def bwd(o):
+        return layer.backward(x, ids, o, dlp, dent) if op == "logprob" else layer.backward(x, ids, t, o, dl)
+
+    saved_way, recomputed = bwd(fwd(True)), bwd(fwd(False))
+    o = fwd(True)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = bwd(o)
+    for _ in range(3):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, recomputed)
+    assert torch.equal(bwd(o), saved_way) and o.saved is None
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, recomputed)
+    del g
+
+
+def test_saved_forward_of_another_stream(lib):
+    """A backward on another stream than its forward's: the saved buffer is not handed out on the
+    forward's stream before the backward has run."""
+    inp = make_head_case(HeadCase("other_stream", 300, 128, 3000, 4, 144))
+    x = dev_bf16(inp["X"])
+    ids, t, dl = up(inp, "ids", "teacher", "dloss")
+    kd = head(lib, inp, lib.LoraDistill)
+    want = kd.backward(x, ids, t, kd.forward(x, ids, t, save=True), dl)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    o = kd.forward(x, ids, t, save=True, stream=s)
+    torch.cuda.synchronize()
+    where, size = o.saved.data_ptr(), o.saved.numel()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s, before the backward in its stream
+    got = kd.backward(x, ids, t, o, dl)
+    with torch.cuda.stream(s):
+        other = torch.empty(size, dtype=torch.uint8, device=x.device)
+    assert other.data_ptr() != where
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("M", [40, 250, 900])
 def test_rows_without_a_gradient_hold_anything(lib, M):
     """NaN hidden states in rows that have no entry (or no upstream gradient) reach neither their own
