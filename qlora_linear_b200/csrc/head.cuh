@@ -64,6 +64,19 @@ __device__ __forceinline__ RowStats join_stats(const RowStats& a, const RowStats
 }
 
 // ---------------------------------------------------------------- one accumulator tile
+// The least of a row's kp group maxima (ord_f32; 0: a group without any yet).
+__device__ __forceinline__ uint32_t head_bound(const unsigned* bound, int kp) {
+  uint32_t low = 0xffffffffu;
+  if (kp >= 4) {
+    for (int j = 0; j < kp; j += 4) {
+      const uint4 b = __ldcg(reinterpret_cast<const uint4*>(bound + j));
+      low = min(min(low, min(b.x, b.y)), min(b.z, b.w));
+    }
+  } else {
+    for (int j = 0; j < kp; ++j) low = min(low, __ldcg(bound + j));
+  }
+  return low;
+}
 // The first n <= 32 accumulators of a chunk (n a multiple of 8) to z.
 __device__ __forceinline__ void head_store_chunk(const uint32_t (&v)[32], int n, float* z) {
 #pragma unroll
@@ -216,17 +229,7 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
   const size_t at = static_cast<size_t>(row) * np + nt;
   const size_t col0 = static_cast<size_t>(row) * V + nt * kHeadTile;
   uint32_t low = 0xffffffffu;
-  if (h.k > 0 && in) {
-    const unsigned* bound = h.bound + static_cast<size_t>(row) * h.kp;
-    if (h.kp >= 4) {
-      for (int j = 0; j < h.kp; j += 4) {
-        const uint4 b = __ldcg(reinterpret_cast<const uint4*>(bound + j));
-        low = min(min(low, min(b.x, b.y)), min(b.z, b.w));
-      }
-    } else {
-      for (int j = 0; j < h.kp; ++j) low = min(low, __ldcg(bound + j));
-    }
-  }
+  if (h.k > 0 && in) low = head_bound(h.bound + static_cast<size_t>(row) * h.kp, h.kp);
   float cm[NC];
   float m = head_tile_max<NC>(tbase, nv, cm);
   uint32_t hits = 0;
@@ -405,6 +408,7 @@ struct HeadRowArgs {
   uint8_t* first;          // [M][tiles]: tokens before each 128-column tile
   float* rowf;             // backward from a saved forward: [M] see head_saved_rows_kernel
   unsigned* bound;         // [M][kp] or null
+  unsigned* live;          // head_rows_kernel's, or null: cleared for the next call
   float4* rowp;            // backward: [M]
   const float* lse;        // [M]
   const float* ent;        // [M] or null
@@ -804,6 +808,7 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
 #pragma unroll
   for (int u = 0; u < kHeadMaxTop / kTopWarps; ++u) push(key[u]);
   cut();
+  if (row == 0 && tid == 0 && a.live != nullptr) *a.live = 0;
   if (tid < a.k) {
     const unsigned long long best = top[tid];
     const size_t at = static_cast<size_t>(row) * a.k + tid;

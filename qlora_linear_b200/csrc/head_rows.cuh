@@ -17,9 +17,21 @@
 //
 // Epilogue: a lane holds one entry's logits of 32 rows.  Sums over the 32 entries of a warp go
 // by transposing reductions (31 shuffles for 32 rows, lane i ending with row i), so a warp keeps the
-// running statistics of row i in lane i, and leaves one partial a CTA, warp and row.  A warp's 32
-// entries are a chunk: with alternatives every chunk's maximum and all logits are written (4·M·V
-// bytes, coalesced).
+// running statistics of row i in lane i, and leaves one partial a CTA, warp and row.
+//
+// Alternatives: a warp's 32 entries are a chunk.  Its maxima are written, and its logits of the rows
+// whose maximum reaches a bound of their k-th largest logit (as the pair kernel's: the least of kp
+// groups' maxima over the chunks seen; a chunk below it has k better ones, so none of its entries is
+// wanted).  The bounds' first values have to come before their first use without a grid barrier or
+// another launch: one warp clears them and sets `live`, a warp that does not see it yet keeps
+// everything and raises nothing, and the row kernel behind clears `live`.  How much is written varies,
+// the results do not.  Once a tile and row a CTA reads the bounds, through shared memory: read by every
+// warp, the 128 bytes a row for k > 16 cost more than the stores saved (48 rows, k = 20: 195 us).  All
+// logits written: 189 us, and 182 so; k = 1: 182 and 172.
+//
+// W's lines leave L2 first (evict_first), so the logits stay for the row kernel: 1 row, k = 8 163 -> 159 us,
+// 8 rows 171 -> 165; with all logits written 48 rows lost 1.5% to it.
+//
 // Roles: warp 0 TMA producer, warp 1 MMA issuer and TMEM owner, warps 2-5 epilogue.  Every wait
 // is bounded.
 #pragma once
@@ -58,11 +70,12 @@ __host__ __device__ constexpr int hr_chunks(long long V) {
 }
 
 struct HeadRowsParams {
-  HeadArgs h;              // sorted and bound are not used; part is [M][4·CTAs]
+  HeadArgs h;              // sorted is not used; part is [M][4·CTAs]
   int cpp;                 // chunks a CTA (cmax is [M][CTAs · cpp])
   const int32_t* ids;      // [M][n]
   int M, V, D;
   int stages;
+  uint32_t* live;          // not 0 once the bounds are cleared
   uint32_t* status;
   uint64_t wait_ns;
 };
@@ -94,6 +107,9 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
   extern __shared__ __align__(1024) uint8_t hr_raw[];
   __shared__ __align__(8) uint64_t full[HR_MAX_STAGES], empty[HR_MAX_STAGES], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot, abort_s, never_s;
+  // bounds of the rows' k-th largest logits (ord_f32); a warp refreshes 32 rows' and reads the others'
+  // as they are: they only rise, an older one keeps more
+  __shared__ uint32_t lows[HR_ROWS];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(hr_raw) + 1023) & ~uintptr_t(1023));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -106,6 +122,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
   const int nkb = (p.D + HR_BK - 1) / HR_BK;
   const WaitCtl wc{&abort_s, p.status, p.wait_ns};
 
+  if (threadIdx.x < HR_ROWS) lows[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -138,6 +155,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
       uint32_t phase = 0;
       long long fills = 0;
       bool ok = true;
+      const uint64_t once = l2_evict_first();
       const int shift = static_cast<int>(static_cast<long long>(blockIdx.x) * nkb / gridDim.x);
       for (int t = 0; ok && t < ntiles; ++t) {
         const int v0 = r0 + t * HR_BN;
@@ -161,7 +179,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (rows & (HR_BN >> i)) {
-                  tma_load_2d(sW + a * (HR_W_BYTES / HR_ATOMS) + u * 128, &tmW.box[i], bar, x, v0 + u);
+                  tma_load_2d_hint(sW + a * (HR_W_BYTES / HR_ATOMS) + u * 128, &tmW.box[i], bar, x, v0 + u, once);
                   u += HR_BN >> i;
                 }
               tma_load_2d(sW + HR_W_BYTES + a * (xbytes / HR_ATOMS), &tmX, bar, x, 0);
@@ -225,6 +243,13 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;
     const HeadArgs& h = p.h;
+    // one warp of the grid clears the bounds
+    if (h.k > 0 && blockIdx.x == 0 && warp == 2) {
+      for (int i = lane; i < p.M * h.kp; i += 32) h.bound[i] = 0u;
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) atomicExch(p.live, 1u);
+    }
     const int np = static_cast<int>(gridDim.x) * HR_WARPS, pi = static_cast<int>(blockIdx.x) * HR_WARPS + quarter;
     constexpr int GROUPS = HR_ROWS / 32;
     RowStats st[GROUPS];  // of row 32·g + lane
@@ -237,8 +262,16 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
+    volatile uint32_t* vlow = lows;
+    bool live = false;
     for (int t = 0; t < ntiles; ++t) {
+      const int mine = quarter * 32 + lane;
+      if (live && mine < p.M) vlow[mine] = head_bound(h.bound + static_cast<size_t>(mine) * h.kp, h.kp);
       if (!mbar_wait_warp(smem_u32(&tfull[acc]), acc_phase, wc)) { ok = false; break; }
+      if (h.k > 0 && !live) {
+        live = __shfl_sync(0xffffffffu, lane == 0 ? ld_acquire_gpu(p.live) : 0u, 0) != 0u;
+        __syncwarp();
+      }
       tc_fence_after();
       const int c0 = r0 + t * HR_BN + quarter * 32;  // the warp's chunk of entries
       const int nc = min(32, min(r1, p.V) - c0);     // <= 0: past the range
@@ -267,18 +300,27 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
             __syncwarp();
           }
         }
-        if (h.k > 0 && valid) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (g * 32 + j < p.M) h.zlog[static_cast<size_t>(g * 32 + j) * p.V + c0 + lane] = __uint_as_float(v[j]);
-        }
+        const uint32_t low = vlow[row];
         float x[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = valid ? __uint_as_float(v[j]) : -INFINITY;
         const float top = transpose_reduce(x, lane, [](float a, float b) { return fmaxf(a, b); });
-        if (h.k > 0 && row < p.M)
-          h.cmax[(static_cast<size_t>(row) * gridDim.x + blockIdx.x) * p.cpp + t * (HR_BN / 32) + quarter] =
-              fmaxf(top, -INFINITY);
+        if (h.k > 0) {
+          const uint32_t o = ord_f32(fmaxf(top, -INFINITY));
+          const bool keep = row < p.M && o >= low;
+          const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+          if (row < p.M)
+            h.cmax[(static_cast<size_t>(row) * gridDim.x + blockIdx.x) * p.cpp + t * (HR_BN / 32) + quarter] =
+                fmaxf(top, -INFINITY);
+          if (live && keep)
+            atomicMax(h.bound + static_cast<size_t>(row) * h.kp + ((blockIdx.x * HR_WARPS + quarter + t) & (h.kp - 1)), o);
+          if (valid) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (kept >> j & 1u)
+                h.zlog[static_cast<size_t>(g * 32 + j) * p.V + c0 + lane] = __uint_as_float(v[j]);
+          }
+        }
         const float m = top * h.c2;
         float y[32];
 #pragma unroll

@@ -30,6 +30,7 @@ namespace {
 constexpr int kTargetCtas = 296;          // skinny passes: about two waves of 148 SMs
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;  // 2 s bound for every device wait
 constexpr size_t kStatusBytes = 256;      // workspace head: device status word
+constexpr int kLiveWord = 32;             // and, of it, head_rows_kernel's word (0 between calls)
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
@@ -1389,6 +1390,7 @@ lora_status_t head_fwd_core(const void* X, long long M, const lora_weight_t* W, 
     p.stages = hr_stages(p.M);
     p.status = status;
     p.wait_ns = wait_limit_ns();
+    if (k > 0) r.live = p.live = status + kLiveWord;
     CUtensorMap tx;
     HeadRowsMaps tw;
     TRY(tmap_bf16(&tx, X, D, M, 64, static_cast<uint32_t>(hr_n(p.M))));

@@ -201,6 +201,32 @@ def test_alternatives_in_hard_orders(lib, M, kind):
     assert layer.status() == lib.LORA_OK
 
 
+@pytest.mark.parametrize("kind", ["random", "ascending", "descending", "peaks", "equal"])
+def test_alternatives_of_few_rows_over_long_ranges(lib, kind):
+    """Several tiles a CTA, so that later chunks are kept or dropped by the bound of earlier ones; calls
+    of other sizes in between on the same workspace."""
+    V, M = 60008, 128
+    inp = make_head_case(HeadCase("long", M, 16, V, 1, 72))
+    W, X = O.bf16_to_f64(inp["W"]), O.bf16_to_f64(inp["X"])
+    if kind != "random":
+        X[:] = 0
+        X[:, 0] = 1
+        X[1::2, 0] = -1  # every other row the other way round
+        v = np.arange(V)
+        W[:] = 0
+        W[:, 0] = {"ascending": v // 512 / 8.0, "descending": -(v // 512) / 8.0, "equal": 0.0 * v,
+                   "peaks": np.where(v % 1009 == 1008, (v // 1009) / 4.0, -1.0)}[kind]
+    ref = O.token_logprobs(X, W, inp["ids"], -100, 1.0, 32)
+    to = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(torch.bfloat16).cuda()  # noqa: E731  (exact)
+    layer = lib.LoraTokenLogProbs(lib.LoraWeight.bf16(to(W)))
+    for m in (128, 1, 33):
+        for k in (32, 1, 5, 20, 2):
+            out = layer.forward(to(X[:m]), None, top_k=k)
+            assert np.array_equal(out.top_ids.cpu().numpy(), ref["top_ids"][:m, :k]), (m, k)
+            close("top_logprob", out.top_logprob, ref["top_logprob"][:m, :k], LP_ATOL)
+    assert layer.status() == lib.LORA_OK
+
+
 @pytest.mark.parametrize("M", [4, 140])
 def test_ids_out_of_range_ignored_and_twice(lib, M):
     inp = make_head_case(HeadCase("ids", M, 64, 520, 4, 81, ignore_frac=0.0))
