@@ -216,13 +216,15 @@ class LoraTokenLogProbs(_HeadLayer):
             raise ValueError(f"top_k must be between 0 and {min(_b.LORA_HEAD_MAX_TOP, self.W.N)}")
 
         def call(handle):
+            # empty_like and sizes as numbers: half of what empty() takes with a shape
             f32 = torch.float32
+            lse = torch.empty(M, dtype=f32, device=dev)
             out = TokenLogProbs(
-                None if ids is None else torch.empty(ids.shape, dtype=f32, device=dev),
-                torch.empty(M, dtype=f32, device=dev),
-                torch.empty(M, dtype=f32, device=dev) if entropy else None,
-                torch.empty((M, k), dtype=torch.int32, device=dev) if k else None,
-                torch.empty((M, k), dtype=f32, device=dev) if k else None,
+                None if ids is None else torch.empty_like(ids, dtype=f32),
+                lse,
+                torch.empty_like(lse) if entropy else None,
+                torch.empty(M, k, dtype=torch.int32, device=dev) if k else None,
+                torch.empty(M, k, dtype=f32, device=dev) if k else None,
                 self._saved(M, n, dev) if save else None, n)
             ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, k), dev, handle)
             _check(_lib.lora_logprob_fwd(X.data_ptr(), M, byref(self.W.c_struct()), _ptr(ids), n, self.ignore_index,
@@ -284,8 +286,8 @@ class LoraDistill(_HeadLayer):
         n = self._teacher(ids, teacher_logits, M, dev)
 
         def call(handle):
-            out = DistillLoss(torch.empty(M, dtype=torch.float32, device=dev),
-                              torch.empty(M, dtype=torch.float32, device=dev), self._saved(M, n, dev) if save else None, n)
+            loss = torch.empty(M, dtype=torch.float32, device=dev)
+            out = DistillLoss(loss, torch.empty_like(loss), self._saved(M, n, dev) if save else None, n)
             ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, 0), dev, handle)
             _check(_lib.lora_distill_fwd(X.data_ptr(), M, byref(self.W.c_struct()), ids.data_ptr(),
                                          teacher_logits.data_ptr(), n, self.ignore_index, self.scale,
