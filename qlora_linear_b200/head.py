@@ -114,8 +114,9 @@ class _HeadLayer:
         key = (device.index, stream)
         ws = self._ws.get(key)
         if ws is None or ws.numel() < nbytes:
+            head = torch.zeros(256, dtype=torch.uint8, device=device) if ws is None else ws[:256]
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            ws[:256].zero_()
+            ws[:256].copy_(head)  # a larger one keeps the status
             self._ws[key] = ws
         return ws
 

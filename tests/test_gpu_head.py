@@ -565,6 +565,18 @@ def test_same_bits_of_compacted_rows(lib):
     assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(runs[0], r))
 
 
+def test_a_larger_workspace_keeps_the_status(lib):
+    inp = make_head_case(HeadCase("status", 300, 64, 3000, 1, 151))
+    x = dev_bf16(inp["X"])
+    layer = head(lib, inp, lib.LoraTokenLogProbs)
+    layer.forward(x[:2])
+    (ws,) = layer._ws.values()
+    ws[:4].view(torch.int32).fill_(1)  # as a kernel that gave up a wait leaves it
+    layer.forward(x, top_k=4)
+    assert layer._ws[next(iter(layer._ws))].numel() > ws.numel()
+    assert layer.status() == lib.LORA_ERR_DEVICE_TIMEOUT and layer.status() == lib.LORA_OK
+
+
 def test_two_threads_on_one_stream(lib):
     import threading
 
