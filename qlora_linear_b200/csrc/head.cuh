@@ -751,8 +751,11 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
       for (int i = 1; i < kTopPer; ++i) c = u == i ? cm[i] : c;
       push(q < chunks ? top_key(c, q) : 0ull);
       if (!fits) {
+        // one decision for the block: read between two barriers, since the next push adds to buf_n
         __syncthreads();
-        if (buf_n > kTopBuf - kTopThreads) cut();
+        const bool full = buf_n > kTopBuf - kTopThreads;
+        __syncthreads();
+        if (full) cut();
       }
     }
     __syncthreads();
