@@ -749,14 +749,15 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
       float c = cm[0];
 #pragma unroll
       for (int i = 1; i < kTopPer; ++i) c = u == i ? cm[i] : c;
-      push(q < chunks ? top_key(c, q) : 0ull);
       if (!fits) {
-        // one decision for the block: read between two barriers, since the next push adds to buf_n
+        // room for what the next push adds, which starts from up to kTopBuf keys of an earlier pass; one
+        // decision for the block, read between two barriers since the push adds to buf_n
         __syncthreads();
         const bool full = buf_n > kTopBuf - kTopThreads;
         __syncthreads();
         if (full) cut();
       }
+      push(q < chunks ? top_key(c, q) : 0ull);
     }
     __syncthreads();
   }
