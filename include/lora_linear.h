@@ -359,9 +359,11 @@ lora_status_t lora_ce_bwd(const void* X, int64_t M, const lora_weight_t* W, cons
  * saved: NULL, or device memory of lora_head_saved_bytes(M, V, n) in which the forward keeps
  * exp(z) in bf16 (2·M·V bytes and a little; rescaled where the type could not hold it) for the
  * backward, which then skips the logits' product, a third of the training step's work.  The
- * backward (same n) works in that buffer: it serves one backward.  With saved == NULL the backward recomputes the
- * logits: over the whole vocabulary at once if the workspace holds dz [M, V], else slice by
- * slice, as lora_ce_bwd.
+ * backward works in that buffer: it serves one backward, of the same operator and the same M, W, ids, n,
+ * ignore_index and scale (the two operators lay the buffer out differently, and distillation's holds
+ * the indices of its rows, which the backward follows unchecked).  With saved == NULL the backward
+ * recomputes the logits: over the whole vocabulary at once if the workspace holds dz [M, V], else slice
+ * by slice, as lora_ce_bwd.
  *
  * Backward: ids, n, ignore_index, scale, X and W as in the forward, lse (and, with dentropy,
  * entropy) from it; dlogprob fp32 [M, n] or NULL, dentropy fp32 [M] or NULL (NULL: zero);

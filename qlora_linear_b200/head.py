@@ -157,6 +157,13 @@ class _HeadLayer:
         self._like(ids, "ids", torch.int32, ids.shape, device)
         return n
 
+    @staticmethod
+    def _own(fwd, cls):
+        """Refuses the other operator's forward: the saved buffers are laid out differently (distillation's
+        holds a map of its rows, which the backward follows)."""
+        if not isinstance(fwd, cls):
+            raise ValueError(f"fwd must be the {cls.__name__} of this operator's forward")
+
     def _slice(self, M):
         """Vocabulary rows a slice of a backward that recomputes: about 1 GiB of dz unless set."""
         if self.slice > 0:
@@ -241,6 +248,7 @@ class LoraTokenLogProbs(_HeadLayer):
                  stream=None) -> torch.Tensor:
         M, dev = self._hidden(X), X.device
         n = 0 if ids is None else self._ids(ids, M, dev, True)
+        self._own(fwd, TokenLogProbs)
         if dlogprob is not None:
             if ids is None:
                 raise ValueError("dlogprob without ids")
@@ -302,6 +310,7 @@ class LoraDistill(_HeadLayer):
                  dloss: torch.Tensor, dX=None, stream=None) -> torch.Tensor:
         M, dev = self._hidden(X), X.device
         n = self._teacher(ids, teacher_logits, M, dev)
+        self._own(fwd, DistillLoss)
         self._like(dloss, "dloss", torch.float32, (M,), dev)
         self._like(fwd.lse, "the forward's lse", torch.float32, (M,), dev)
 

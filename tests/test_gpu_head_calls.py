@@ -1,0 +1,29 @@
+"""GPU tests of calls of the LM head's layers that come out of order, between streams and graphs, or
+after other calls of the same layer: they give the results of the call alone, or are refused."""
+import pytest
+import torch
+
+from synth import HeadCase, make_head_case
+from tests.gpu_helpers import dev_bf16
+from tests.test_gpu_head import head, up
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("save", [False, True])
+def test_a_forward_of_the_other_operator_is_refused(lib, save):
+    """Before anything runs, and the saved forward still serves its own backward.  (8 rows: at this
+    size neither operator's buffer holds a map of rows.)"""
+    inp = make_head_case(HeadCase("swap", 8, 64, 256, 2, 301))
+    lp, kd = head(lib, inp, lib.LoraTokenLogProbs), head(lib, inp, lib.LoraDistill)
+    x = dev_bf16(inp["X"])
+    ids, t, dl, dlp = up(inp, "ids", "teacher", "dloss", "dlogprob")
+    o, d = lp.forward(x, ids, save=save), kd.forward(x, ids, t, save=save)
+    with pytest.raises(ValueError):
+        kd.backward(x, ids, t, o, dl)
+    with pytest.raises(ValueError):
+        lp.backward(x, ids, d, dlp)
+    assert (o.saved is not None) == save and (d.saved is not None) == save
+    a, b = lp.backward(x, ids, o, dlp), kd.backward(x, ids, t, d, dl)
+    assert torch.equal(a, lp.backward(x, ids, lp.forward(x, ids, save=save), dlp))
+    assert torch.equal(b, kd.backward(x, ids, t, kd.forward(x, ids, t, save=save), dl))
