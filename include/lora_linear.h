@@ -482,6 +482,14 @@ lora_status_t lora_linear_fwd_noalloc(const void* X, int64_t M, const lora_weigh
  */
 lora_status_t lora_device_status(void* workspace, void* stream);
 
+/*
+ * *id (host memory): the same number for every call of one graph capture that `stream` takes part in,
+ * another one for each capture, 0 while `stream` is not captured.  A buffer that one backward uses up
+ * serves a captured one only if the forward that fills it is part of the same capture: two graphs may
+ * be replayed a different number of times.
+ */
+lora_status_t lora_stream_capture_id(void* stream, uint64_t* id);
+
 /* Static message for a status code (never NULL). */
 const char* lora_status_string(int32_t status);
 

@@ -46,7 +46,7 @@ EXPORTED = (
     "lora_testing_tcproj_extra_tile", "lora_testing_tcproj_splits",
     "lora_head_fwd_workspace_bytes", "lora_head_bwd_workspace_bytes", "lora_head_saved_bytes",
     "lora_logprob_fwd", "lora_logprob_bwd", "lora_distill_fwd", "lora_distill_bwd",
-    "lora_testing_head_splits",
+    "lora_testing_head_splits", "lora_stream_capture_id",
 )
 
 LORA_HEAD_MAX_IDS = 128  # given tokens (or teacher entries) a row
@@ -151,6 +151,8 @@ def _load() -> ctypes.CDLL:
     lib.lora_merge.restype = i32
     lib.lora_device_status.argtypes = [vp, vp]
     lib.lora_device_status.restype = i32
+    lib.lora_stream_capture_id.argtypes = [vp, ctypes.POINTER(ctypes.c_uint64)]
+    lib.lora_stream_capture_id.restype = i32
     lib.lora_status_string.argtypes = [i32]
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_version.argtypes = []
@@ -324,6 +326,13 @@ def lora_merge(W: LoraWeight, A, B, r: int, s: float, W_out, stream=None) -> Non
 
 def lora_device_status(workspace, stream=None) -> int:
     return int(_lib.lora_device_status(_ptr(workspace), _stream(stream)))
+
+
+def lora_stream_capture_id(stream=None) -> int:
+    """The graph capture that the stream takes part in, 0 for none."""
+    capture = ctypes.c_uint64(0)
+    _check(_lib.lora_stream_capture_id(_stream(stream), ctypes.byref(capture)), "lora_stream_capture_id")
+    return capture.value
 
 
 def lora_testing_bounded_wait(workspace, limit_ns: int, stream=None) -> int:

@@ -2053,6 +2053,15 @@ lora_status_t lora_device_status(void* workspace, void* stream) {
   return (word & kDevErrTimeout) ? LORA_ERR_DEVICE_TIMEOUT : LORA_ERR_CUDA;
 }
 
+lora_status_t lora_stream_capture_id(void* stream, uint64_t* id) {
+  if (!id) return LORA_ERR_INVALID_ARG;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long capture = 0;
+  if (cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &capture) != cudaSuccess) return LORA_ERR_CUDA;
+  *id = status == cudaStreamCaptureStatusNone ? 0 : capture;
+  return LORA_OK;
+}
+
 lora_status_t lora_testing_bounded_wait(void* workspace, uint64_t limit_ns, void* stream) {
   if (!workspace) return LORA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return LORA_ERR_ALIGNMENT;

@@ -40,7 +40,7 @@ class TokenLogProbs:
     saved: torch.Tensor | None = None
     tokens: int = 0
     stream: int = 0         # the stream that saved was taken on
-    captured: bool = False  # the forward ran under graph capture
+    capture: int = 0        # the graph capture that the forward was part of, 0: none
 
 
 @dataclasses.dataclass
@@ -53,7 +53,7 @@ class DistillLoss:
     saved: torch.Tensor | None = None
     tokens: int = 0
     stream: int = 0         # the stream that saved was taken on
-    captured: bool = False  # the forward ran under graph capture
+    capture: int = 0        # the graph capture that the forward was part of, 0: none
 
 
 class _HeadLayer:
@@ -174,10 +174,10 @@ class _HeadLayer:
         return torch.empty(self._bytes(_b.head_saved_bytes, M, self.W.N, n), dtype=torch.uint8, device=device)
 
     def _take_saved(self, fwd, M, n, stream):
-        """The forward's saved buffer for this backward, which overwrites it (None: recompute).  A
-        captured backward runs on every replay, so it leaves the buffer of a forward that does not
-        run with it alone."""
-        if fwd.saved is None or (not fwd.captured and torch.cuda.is_current_stream_capturing()):
+        """The forward's saved buffer for this backward, which overwrites it (None: recompute).  It
+        serves a backward that runs once for each run of the forward: both ordinary calls, or both in
+        one graph."""
+        if fwd.saved is None or fwd.capture != self._capture(stream):
             return None
         saved, fwd.saved = fwd.saved, None
         if fwd.tokens != n or saved.numel() != self._bytes(_b.head_saved_bytes, M, self.W.N, n):
@@ -187,9 +187,13 @@ class _HeadLayer:
         return saved
 
     @staticmethod
-    def _mark(out, stream):
+    def _capture(stream):
+        return _b.lora_stream_capture_id(stream) if torch.cuda.is_current_stream_capturing() else 0
+
+    @classmethod
+    def _mark(cls, out, stream):
         if out.saved is not None:
-            out.stream, out.captured = stream, torch.cuda.is_current_stream_capturing()
+            out.stream, out.capture = stream, cls._capture(stream)
         return out
 
     def _bwd_workspace(self, M, n, saved, device, handle):
@@ -210,9 +214,10 @@ class LoraTokenLogProbs(_HeadLayer):
     ``forward(X, ids)``: X bf16 [M, D], ids int32 [M] or [M, n] (n <= 128, entries equal to
     ``ignore_index`` have logprob 0 and no gradient) or None; top_k <= 32.  With ``save=True`` the
     forward keeps 2·M·V bytes for one backward, which then skips recomputing the logits (a later
-    backward of the same forward, or one captured into a graph without it, recomputes them, in
-    vocabulary slices of ``slice_`` rows, by default as many as take 1 GiB).  ``backward`` returns dX for upstream gradients of the
-    log-probabilities (shape of ids) and of the entropies ([M]).
+    backward of the same forward, or one of which only either was captured into a graph, or each into
+    its own, recomputes them, in vocabulary slices of ``slice_`` rows, by default as many as take 1 GiB).
+    ``backward`` returns dX for upstream gradients of the log-probabilities (shape of ids) and of the
+    entropies ([M]).
     """
 
     def forward(self, X: torch.Tensor, ids: torch.Tensor | None = None, top_k: int = 0, entropy: bool = True,

@@ -27,3 +27,44 @@ def test_a_forward_of_the_other_operator_is_refused(lib, save):
     a, b = lp.backward(x, ids, o, dlp), kd.backward(x, ids, t, d, dl)
     assert torch.equal(a, lp.backward(x, ids, lp.forward(x, ids, save=save), dlp))
     assert torch.equal(b, kd.backward(x, ids, t, kd.forward(x, ids, t, save=save), dl))
+
+
+@pytest.mark.parametrize("op", ["logprob", "distill"])
+def test_forward_and_backward_in_two_graphs(lib, op):
+    """A backward captured into another graph than its forward recomputes the logits, so each of its
+    replays gives the gradient, however often the forward was replayed before; so does an ordinary
+    backward of a captured forward.  In one graph the saved forward serves."""
+    inp = make_head_case(HeadCase("two_graphs", 300, 128, 3000, 4, 311))
+    x = dev_bf16(inp["X"])
+    ids, t, dl, dlp, dent = up(inp, "ids", "teacher", "dloss", "dlogprob", "dentropy")
+    layer = head(lib, inp, lib.LoraTokenLogProbs if op == "logprob" else lib.LoraDistill)
+
+    def fwd(save):
+        return layer.forward(x, ids, save=save) if op == "logprob" else layer.forward(x, ids, t, save=save)
+
+    def bwd(o):
+        return layer.backward(x, ids, o, dlp, dent) if op == "logprob" else layer.backward(x, ids, t, o, dl)
+
+    saved_way, recomputed = bwd(fwd(True)), bwd(fwd(False))
+    assert not torch.equal(saved_way, recomputed)
+    torch.cuda.synchronize()
+    a, b, both = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(a):
+        o = fwd(True)
+    with torch.cuda.graph(b):
+        got = bwd(o)
+    with torch.cuda.graph(both):
+        together = bwd(fwd(True))
+    for replays in (1, 3, 2):
+        a.replay()
+        for _ in range(replays):
+            got.zero_()
+            b.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, recomputed)
+        assert torch.equal(bwd(o), recomputed) and torch.equal(bwd(o), recomputed)
+        together.zero_()
+        both.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(together, saved_way)
+    del a, b, both
