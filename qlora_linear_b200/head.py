@@ -107,6 +107,8 @@ class _HeadLayer:
         return n
 
     def _workspace(self, nbytes: int, device, stream: int) -> torch.Tensor:
+        """At least nbytes.  A call passes the library the size that it asked for, not the buffer's: the
+        backward's slices go by it."""
         if torch.cuda.is_current_stream_capturing():
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
             ws[:256].zero_()
@@ -196,9 +198,9 @@ class _HeadLayer:
             out.stream, out.capture = stream, cls._capture(stream)
         return out
 
-    def _bwd_workspace(self, M, n, saved, device, handle):
+    def _bwd_bytes(self, M, n, saved) -> int:
         slice_ = 0 if saved is not None else self._slice(M)
-        return self._workspace(self._bytes(_b.head_bwd_workspace_bytes, M, self.W.K, self.W.N, n, slice_), device, handle)
+        return self._bytes(_b.head_bwd_workspace_bytes, M, self.W.K, self.W.N, n, slice_)
 
     def _dX(self, dX, X):
         if dX is None:
@@ -239,11 +241,12 @@ class LoraTokenLogProbs(_HeadLayer):
                 torch.empty(M, k, dtype=torch.int32, device=dev) if k else None,
                 torch.empty(M, k, dtype=f32, device=dev) if k else None,
                 self._saved(M, n, dev) if save else None, n)
-            ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, k), dev, handle)
+            size = self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, k)
+            ws = self._workspace(size, dev, handle)
             _check(_lib.lora_logprob_fwd(X.data_ptr(), M, byref(self.W.c_struct()), _ptr(ids), n, self.ignore_index,
                                          self.scale, k, _ptr(out.logprob), _ptr(out.entropy), out.lse.data_ptr(),
                                          _ptr(out.top_ids), _ptr(out.top_logprob), _ptr(out.saved), ws.data_ptr(),
-                                         ws.numel(), handle), "lora_logprob_fwd")
+                                         size, handle), "lora_logprob_fwd")
             return self._mark(out, handle)
 
         return self._run(call, X, stream, ids)
@@ -267,10 +270,11 @@ class LoraTokenLogProbs(_HeadLayer):
         def call(handle):
             out = self._dX(dX, X)
             saved = self._take_saved(fwd, M, n, handle)
-            ws = self._bwd_workspace(M, n, saved, dev, handle)
+            size = self._bwd_bytes(M, n, saved)
+            ws = self._workspace(size, dev, handle)
             _check(_lib.lora_logprob_bwd(X.data_ptr(), M, byref(self.W.c_struct()), _ptr(ids), n, self.ignore_index,
                                          self.scale, fwd.lse.data_ptr(), _ptr(fwd.entropy), _ptr(dlogprob),
-                                         _ptr(dentropy), _ptr(saved), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                         _ptr(dentropy), _ptr(saved), out.data_ptr(), ws.data_ptr(), size,
                                          handle), "lora_logprob_bwd")
             return out
 
@@ -302,11 +306,12 @@ class LoraDistill(_HeadLayer):
         def call(handle):
             loss = torch.empty(M, dtype=torch.float32, device=dev)
             out = DistillLoss(loss, torch.empty_like(loss), self._saved(M, n, dev) if save else None, n)
-            ws = self._workspace(self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, 0), dev, handle)
+            size = self._bytes(_b.head_fwd_workspace_bytes, M, self.W.K, self.W.N, n, 0)
+            ws = self._workspace(size, dev, handle)
             _check(_lib.lora_distill_fwd(X.data_ptr(), M, byref(self.W.c_struct()), ids.data_ptr(),
                                          teacher_logits.data_ptr(), n, self.ignore_index, self.scale,
                                          out.loss.data_ptr(), out.lse.data_ptr(), _ptr(out.saved), ws.data_ptr(),
-                                         ws.numel(), handle), "lora_distill_fwd")
+                                         size, handle), "lora_distill_fwd")
             return self._mark(out, handle)
 
         return self._run(call, X, stream, ids, teacher_logits)
@@ -322,11 +327,12 @@ class LoraDistill(_HeadLayer):
         def call(handle):
             out = self._dX(dX, X)
             saved = self._take_saved(fwd, M, n, handle)
-            ws = self._bwd_workspace(M, n, saved, dev, handle)
+            size = self._bwd_bytes(M, n, saved)
+            ws = self._workspace(size, dev, handle)
             _check(_lib.lora_distill_bwd(X.data_ptr(), M, byref(self.W.c_struct()), ids.data_ptr(),
                                          teacher_logits.data_ptr(), n, self.ignore_index, self.scale,
                                          fwd.lse.data_ptr(), dloss.data_ptr(), _ptr(saved), out.data_ptr(),
-                                         ws.data_ptr(), ws.numel(), handle), "lora_distill_bwd")
+                                         ws.data_ptr(), size, handle), "lora_distill_bwd")
             return out
 
         return self._run(call, X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved)

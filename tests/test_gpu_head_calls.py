@@ -68,3 +68,40 @@ def test_forward_and_backward_in_two_graphs(lib, op):
         torch.cuda.synchronize()
         assert torch.equal(together, saved_way)
     del a, b, both
+
+
+@pytest.mark.parametrize("op", ["logprob", "distill"])
+def test_slices_are_those_of_the_call_whatever_ran_before(lib, op):
+    """The slices of a backward that recomputes go by the layer's slice_, not by what a larger call
+    left as its workspace: the same bits before and after one, and in a graph."""
+    inp = make_head_case(HeadCase("grown", 300, 128, 5000, 4, 321))
+    x = dev_bf16(inp["X"])
+    ids, t, dl, dlp, dent = up(inp, "ids", "teacher", "dloss", "dlogprob", "dentropy")
+    W = lib.LoraWeight.bf16(dev_bf16(inp["W"]))
+    cls = lib.LoraTokenLogProbs if op == "logprob" else lib.LoraDistill
+
+    def bwd(layer, o):
+        return layer.backward(x, ids, o, dlp, dent) if op == "logprob" else layer.backward(x, ids, t, o, dl)
+
+    whole = cls(W)
+    o = whole.forward(x, ids) if op == "logprob" else whole.forward(x, ids, t)
+    one_piece = bwd(whole, o)
+    layer = cls(W, slice_=256)
+    want = bwd(layer, o)
+    assert not torch.equal(want, one_piece)
+    before = sum(ws.numel() for ws in layer._ws.values())
+    big = x.repeat(8, 1)
+    if op == "logprob":
+        layer.forward(big, None, top_k=32)
+    else:
+        layer.forward(big, ids.repeat(8, 1), t.repeat(8, 1))
+    assert sum(ws.numel() for ws in layer._ws.values()) > before
+    assert torch.equal(bwd(layer, o), want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = bwd(layer, o)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    del g
