@@ -175,18 +175,23 @@ class _HeadLayer:
     def _saved(self, M, n, device):
         return torch.empty(self._bytes(_b.head_saved_bytes, M, self.W.N, n), dtype=torch.uint8, device=device)
 
-    def _take_saved(self, fwd, M, n, stream):
-        """The forward's saved buffer for this backward, which overwrites it (None: recompute).  It
-        serves a backward that runs once for each run of the forward: both ordinary calls, or both in
-        one graph."""
+    def _saved_of(self, fwd, M, n, stream):
+        """The forward's saved buffer for this backward, which overwrites it (None: recompute); _used
+        drops it once the call has been made.  It serves a backward that runs once for each run of the
+        forward: both ordinary calls, or both in one graph."""
         if fwd.saved is None or fwd.capture != self._capture(stream):
             return None
-        saved, fwd.saved = fwd.saved, None
+        saved = fwd.saved
         if fwd.tokens != n or saved.numel() != self._bytes(_b.head_saved_bytes, M, self.W.N, n):
             raise ValueError("the forward was saved with other sizes (rows, tokens a row or vocabulary)")
         if fwd.stream != stream:  # not handed out again before this backward has run
             saved.record_stream(torch.cuda.current_stream())
         return saved
+
+    @staticmethod
+    def _used(fwd, saved):
+        if saved is not None:
+            fwd.saved = None
 
     @staticmethod
     def _capture(stream):
@@ -269,13 +274,14 @@ class LoraTokenLogProbs(_HeadLayer):
 
         def call(handle):
             out = self._dX(dX, X)
-            saved = self._take_saved(fwd, M, n, handle)
+            saved = self._saved_of(fwd, M, n, handle)
             size = self._bwd_bytes(M, n, saved)
             ws = self._workspace(size, dev, handle)
             _check(_lib.lora_logprob_bwd(X.data_ptr(), M, byref(self.W.c_struct()), _ptr(ids), n, self.ignore_index,
                                          self.scale, fwd.lse.data_ptr(), _ptr(fwd.entropy), _ptr(dlogprob),
                                          _ptr(dentropy), _ptr(saved), out.data_ptr(), ws.data_ptr(), size,
                                          handle), "lora_logprob_bwd")
+            self._used(fwd, saved)
             return out
 
         return self._run(call, X, stream, ids, dlogprob, dentropy, fwd.lse, fwd.entropy, fwd.saved)
@@ -326,13 +332,14 @@ class LoraDistill(_HeadLayer):
 
         def call(handle):
             out = self._dX(dX, X)
-            saved = self._take_saved(fwd, M, n, handle)
+            saved = self._saved_of(fwd, M, n, handle)
             size = self._bwd_bytes(M, n, saved)
             ws = self._workspace(size, dev, handle)
             _check(_lib.lora_distill_bwd(X.data_ptr(), M, byref(self.W.c_struct()), ids.data_ptr(),
                                          teacher_logits.data_ptr(), n, self.ignore_index, self.scale,
                                          fwd.lse.data_ptr(), dloss.data_ptr(), _ptr(saved), out.data_ptr(),
                                          ws.data_ptr(), size, handle), "lora_distill_bwd")
+            self._used(fwd, saved)
             return out
 
         return self._run(call, X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved)

@@ -105,3 +105,23 @@ def test_slices_are_those_of_the_call_whatever_ran_before(lib, op):
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     del g
+
+
+def test_a_refused_backward_keeps_the_saved_forward(lib):
+    """Other sizes than the forward's, a tensor that does not start on 16 bytes: the call is refused and
+    the saved forward still serves the right one."""
+    inp = make_head_case(HeadCase("refused", 300, 64, 1000, 2, 331))
+    x = dev_bf16(inp["X"])
+    ids, dlp = up(inp, "ids", "dlogprob")
+    layer = head(lib, inp, lib.LoraTokenLogProbs)
+    want = layer.backward(x, ids, layer.forward(x, ids, save=True), dlp)
+    o = layer.forward(x, ids, save=True)
+    with pytest.raises(ValueError):
+        layer.backward(x, ids[:, 0].contiguous(), o, dlp[:, 0].contiguous())
+    assert o.saved is not None
+    off = torch.empty(601, dtype=torch.int32, device="cuda")[1:].view(300, 2)
+    off.copy_(ids)
+    with pytest.raises(lib.LoraError):
+        layer.backward(x, off, o, dlp)
+    assert o.saved is not None
+    assert torch.equal(layer.backward(x, ids, o, dlp), want) and o.saved is None
