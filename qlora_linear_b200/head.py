@@ -77,8 +77,9 @@ class _HeadLayer:
         self._sizes = {}
         self._lock = threading.Lock()
 
-    def _run(self, call, X, stream, *inputs):
-        """``call(handle)`` with X's device and ``stream`` current; returns what it returns."""
+    def _run(self, call, X, stream, *tensors):
+        """``call(handle)`` with X's device and ``stream`` current; returns what it returns.  The caller's
+        tensors and the head keep their memory until a call on another stream has run."""
         index = X.device.index
         if stream is None and index == torch.cuda.current_device():
             with self._lock:
@@ -89,7 +90,7 @@ class _HeadLayer:
             elif stream is None:
                 stream = torch.cuda.current_stream()
             if stream != torch.cuda.current_stream():
-                for t in (X, *inputs):
+                for t in (X, self.W.data, *tensors):
                     if t is not None:
                         t.record_stream(stream)
             with torch.cuda.stream(stream), self._lock:
@@ -284,7 +285,7 @@ class LoraTokenLogProbs(_HeadLayer):
             self._used(fwd, saved)
             return out
 
-        return self._run(call, X, stream, ids, dlogprob, dentropy, fwd.lse, fwd.entropy, fwd.saved)
+        return self._run(call, X, stream, ids, dlogprob, dentropy, fwd.lse, fwd.entropy, fwd.saved, dX)
 
 
 class LoraDistill(_HeadLayer):
@@ -342,4 +343,4 @@ class LoraDistill(_HeadLayer):
             self._used(fwd, saved)
             return out
 
-        return self._run(call, X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved)
+        return self._run(call, X, stream, ids, teacher_logits, dloss, fwd.lse, fwd.saved, dX)

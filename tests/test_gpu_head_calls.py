@@ -125,3 +125,37 @@ def test_a_refused_backward_keeps_the_saved_forward(lib):
         layer.backward(x, off, o, dlp)
     assert o.saved is not None
     assert torch.equal(layer.backward(x, ids, o, dlp), want) and o.saved is None
+
+
+@pytest.mark.parametrize("what", ["dX", "head"])
+def test_tensors_of_another_stream_are_kept_until_the_call_has_run(lib, what):
+    """A caller's dX and the head, dropped by the caller right after a call on another stream: their
+    memory is not handed out before that call has run."""
+    inp = make_head_case(HeadCase("drop", 300, 136, 3000, 4, 341))
+    x = dev_bf16(inp["X"])
+    ids, t, dl = up(inp, "ids", "teacher", "dloss")
+    layer = head(lib, inp, lib.LoraDistill)
+    s = torch.cuda.Stream()
+    o = layer.forward(x, ids, t)
+    torch.cuda.synchronize()
+    # a workspace of the stream, so that the call itself takes nothing large from the allocator
+    want = layer.backward(x, ids, t, o, dl, stream=s)
+    torch.cuda.synchronize()
+    dX = torch.empty_like(x)
+    torch.cuda.synchronize()
+    kept = dX if what == "dX" else layer.W.data
+    where, shape = kept.data_ptr(), kept.shape
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s, before the backward in its stream
+    got = layer.backward(x, ids, t, o, dl, dX=dX, stream=s)
+    assert got is dX
+    del kept, got
+    if what == "dX":
+        del dX
+    else:
+        del layer
+    other = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    assert all(a.data_ptr() != where for a in other)
+    torch.cuda.synchronize()
+    if what == "head":
+        assert torch.equal(dX, want)
