@@ -127,10 +127,11 @@ class _HeadLayer:
         """The first device status that is not LORA_OK of the calls made so far (synchronizes),
         calls under graph capture aside."""
         out = _b.LORA_OK
-        for (dev, stream), ws in self._ws.items():
-            with torch.cuda.device(dev):
-                st = _b.lora_device_status(ws, stream)
-            out = st if out == _b.LORA_OK else out
+        with self._lock:  # another thread's call may add or replace a workspace
+            for (dev, stream), ws in self._ws.items():
+                with torch.cuda.device(dev):
+                    st = _b.lora_device_status(ws, stream)
+                out = st if out == _b.LORA_OK else out
         return out
 
     def _hidden(self, X):
