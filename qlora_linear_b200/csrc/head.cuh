@@ -49,6 +49,12 @@ __device__ __forceinline__ unsigned long long top_key(float z, int id) {
   return (static_cast<unsigned long long>(ord_f32(z)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
 }
 
+// A maximum of accumulators in units of log 2, rounded.  The sums beside it are relative to this
+// value, so a join has to take it too: an fma of the product with the difference that follows (the
+// compiler's choice for a plain `*`) shifts a tile by the rounding, half an ulp of m (logits around 100:
+// 5e-6 in the log-probability of a certain token).
+__device__ __forceinline__ float head_max_y(float raw, float c2) { return __fmul_rn(raw, c2); }
+
 struct RowStats {
   float m, s, t;  // max y, Σ 2^{y-m}, Σ (y-m)·2^{y-m}
 };
@@ -248,7 +254,7 @@ __device__ __forceinline__ void head_fwd_tile(const HeadArgs& h, uint32_t tbase,
   if (h.n > 0) head_tile_ids(h, tbase, nv, nt * kHeadTile, row, first);
   __syncwarp();
   const float raw = m;
-  m *= h.c2;
+  m = head_max_y(m, h.c2);
   const bool keep = h.expz != nullptr;
   const float tau = m < -43.0f || m > 86.0f ? m : 0.0f;
   const float f = ex2_approx(m - tau);
@@ -577,12 +583,12 @@ __global__ void __launch_bounds__(32 * kHeadRowWarps) head_finalize_kernel(const
   const float4* part = a.part + static_cast<size_t>(slot) * a.np;
   float m = -INFINITY;
   for (int i = lane; i < a.np; i += 32) m = fmaxf(m, part[i].x);
-  m = warp_max(m) * a.c2;
+  m = head_max_y(warp_max(m), a.c2);
   float s = 0.0f, t = 0.0f;
   for (int i = lane; i < a.np; i += 32) {
     const float4 q = part[i];
     if (q.y == 0.0f) continue;  // no entries
-    const float d = q.x * a.c2 - m, e = exp2f(d);
+    const float d = head_max_y(q.x, a.c2) - m, e = exp2f(d);
     s = fmaf(q.y, e, s);
     t = fmaf(fmaf(d, q.y, q.z), e, t);
   }
@@ -673,7 +679,7 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
     m = fmaxf(m, red[u][0]);
     g = fmaxf(g, groups[u][lane]);
   }
-  m *= a.c2;
+  m = head_max_y(m, a.c2);
   float low;
   if (a.ctas > 0) {
     for (int o = 1; o < a.kp; o <<= 1) g = fminf(g, __shfl_xor_sync(0xffffffffu, g, o));
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
   float s = 0.0f, t = 0.0f;
   auto join = [&](const float4& q) {
     if (q.y == 0.0f) return;  // no entries
-    const float d = q.x * a.c2 - m, e = exp2f(d);
+    const float d = head_max_y(q.x, a.c2) - m, e = exp2f(d);
     s = fmaf(q.y, e, s);
     t = fmaf(fmaf(d, q.y, q.z), e, t);
   };

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(HR_THREADS, 1)
                 h.zlog[static_cast<size_t>(g * 32 + j) * p.V + c0 + lane] = __uint_as_float(v[j]);
           }
         }
-        const float m = top * h.c2;
+        const float m = head_max_y(top, h.c2);
         float y[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
