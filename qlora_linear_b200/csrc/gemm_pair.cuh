@@ -326,12 +326,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<B_MN>::templ
       const uint32_t tbase =
           tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * C::BN);
       // the accumulator may be overwritten: the head's epilogues call it once their columns are in
-      // registers, with an arrive that does not wait for the last tile's global stores
+      // registers, with an arrive that orders the TMEM reads alone and so does not wait for the last
+      // tile's global stores
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if constexpr (HEAD) mbar_arrive_cluster_cta(mapa_shared(smem_u32(&tempty[acc]), 0));
+          if constexpr (HEAD) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[acc]), 0));
           else mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
         }
       };

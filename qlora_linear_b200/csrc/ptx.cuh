@@ -176,10 +176,11 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// As above without waiting for this thread's global stores (release at CTA scope): for barriers
-// that hand over TMEM alone, whose reads tcgen05.wait::ld has completed.
-__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// As above, ordering nothing but the tcgen05 operations before a tcgen05.fence::before_thread_sync
+// (and so not waiting for this thread's global stores): for barriers that hand over TMEM alone, whose
+// reads tcgen05.wait::ld has completed.  The scope is the cluster, as the waiting CTA may be the other.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
