@@ -832,7 +832,9 @@ __global__ void __launch_bounds__(kTopThreads) head_finalize_top_kernel(const He
 //   rowf = -scale·C·e^{-lse}: the saved e^z stand, but for tiles that kept 2^{y-tau} (rare: times
 //     2^tau) and the given tokens, which become dz/rowf from their fp32 logits.
 //   rowf = 1 (an entropy gradient, C small against Σ|c|, an lse that e^z cannot hold): the whole
-//     row becomes dz = scale·(Σ c - p·(Σc + g_H·(log p + H))); bound by HBM, 4·V bytes a row.
+//     row becomes dz = scale·(Σ c - p·(Σc + g_H·(log p + H))); bound by HBM, 4·V bytes a row.  Here
+//     dz is rounded to bf16 a second time and takes log p from the rounded e^z (off by up to 2^-8):
+//     the saved buffer has no more, and the GEMM's operand is bf16 in any case.
 //   rowf = 0: nothing, the GEMM's row is 0.
 // A block takes `per` <= 8 rows, a warp each for their tokens, and writes out its whole rows one
 // after the other; more rows a block where there are blocks enough (per = 1 for 13653 rows x 408

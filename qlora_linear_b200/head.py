@@ -1,6 +1,7 @@
-"""Layers over a frozen bf16 LM head that never hold the [M, V] logits: log-probabilities of
+"""Layers over a frozen bf16 LM head that do not write the [M, V] logits: log-probabilities of
 given tokens with entropy and top alternatives, and distillation from a teacher's top logits,
-each with its gradient in the hidden states."""
+each with its gradient in the hidden states.  (A forward with ``save=True`` keeps their exponentials
+in bf16 for the backward.)"""
 from __future__ import annotations
 
 import dataclasses
@@ -218,10 +219,11 @@ class _HeadLayer:
 class LoraTokenLogProbs(_HeadLayer):
     """Log-probabilities of given tokens under softmax(X·Wᵀ/temperature), with the entropy of
     each row and its ``top_k`` alternatives, over a frozen bf16 LM head ``W [V, D]`` (a
-    :class:`LoraWeight`), without the ``[M, V]`` logits.
+    :class:`LoraWeight`), without writing the ``[M, V]`` logits.
 
     ``forward(X, ids)``: X bf16 [M, D], ids int32 [M] or [M, n] (n <= 128, entries equal to
-    ``ignore_index`` have logprob 0 and no gradient) or None; top_k <= 32.  With ``save=True`` the
+    ``ignore_index`` have logprob 0 and no gradient) or None; top_k <= 32 (its workspace, up to 1.25 GiB,
+    stays with the layer, one a stream).  With ``save=True`` the
     forward keeps 2·M·V bytes for one backward, which then skips recomputing the logits (a later
     backward of the same forward, or one of which only either was captured into a graph, or each into
     its own, recomputes them, in vocabulary slices of ``slice_`` rows, by default as many as take 1 GiB).
@@ -292,12 +294,13 @@ class LoraTokenLogProbs(_HeadLayer):
 class LoraDistill(_HeadLayer):
     """Distillation from a teacher's top logits: per row, KL(q || softmax(X·Wᵀ/temperature))
     with q the softmax of the listed teacher logits over the same temperature, over a frozen bf16
-    LM head ``W [V, D]``, without the ``[M, V]`` logits.
+    LM head ``W [V, D]``, without writing the ``[M, V]`` logits.
 
     ``forward(X, ids, teacher_logits)``: X bf16 [M, D]; ids int32 [M, n] and teacher_logits fp32
     [M, n] (n <= 128; log-probabilities serve as well, e.g. the ``top_ids`` and ``top_logprob`` of
-    :class:`LoraTokenLogProbs` on the teacher's head).  Entries whose id is ``ignore_index`` are left
-    out; a row without any has loss 0 and no gradient.  ``save`` and ``slice_`` as for
+    :class:`LoraTokenLogProbs` on the teacher's head with temperature 1: the temperature is applied
+    here).  Entries whose id is ``ignore_index`` are left out; a row without any has loss 0 and no
+    gradient.  ``save`` and ``slice_`` as for
     :class:`LoraTokenLogProbs`.  ``backward`` returns the gradient of Σ dloss·loss in X.
     """
 
