@@ -210,10 +210,9 @@ class _HeadLayer:
         slice_ = 0 if saved is not None else self._slice(M)
         return self._bytes(_b.head_bwd_workspace_bytes, M, self.W.K, self.W.N, n, slice_)
 
-    def _dX(self, dX, X):
-        if dX is None:
-            return torch.empty_like(X)
-        return self._like(dX, "dX", torch.bfloat16, X.shape, X.device)
+    def _check_dX(self, dX, X):
+        if dX is not None:
+            self._like(dX, "dX", torch.bfloat16, X.shape, X.device)
 
 
 class LoraTokenLogProbs(_HeadLayer):
@@ -275,9 +274,10 @@ class LoraTokenLogProbs(_HeadLayer):
                 raise ValueError("dentropy needs a forward with entropy=True")
             self._like(dentropy, "dentropy", torch.float32, (M,), dev)
         self._like(fwd.lse, "the forward's lse", torch.float32, (M,), dev)
+        self._check_dX(dX, X)
 
         def call(handle):
-            out = self._dX(dX, X)
+            out = torch.empty_like(X) if dX is None else dX
             saved = self._saved_of(fwd, M, n, handle)
             size = self._bwd_bytes(M, n, saved)
             ws = self._workspace(size, dev, handle)
@@ -334,9 +334,10 @@ class LoraDistill(_HeadLayer):
         self._own(fwd, DistillLoss)
         self._like(dloss, "dloss", torch.float32, (M,), dev)
         self._like(fwd.lse, "the forward's lse", torch.float32, (M,), dev)
+        self._check_dX(dX, X)
 
         def call(handle):
-            out = self._dX(dX, X)
+            out = torch.empty_like(X) if dX is None else dX
             saved = self._saved_of(fwd, M, n, handle)
             size = self._bwd_bytes(M, n, saved)
             ws = self._workspace(size, dev, handle)

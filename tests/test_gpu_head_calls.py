@@ -159,3 +159,18 @@ def test_tensors_of_another_stream_are_kept_until_the_call_has_run(lib, what):
     torch.cuda.synchronize()
     if what == "head":
         assert torch.equal(dX, want)
+
+
+def test_a_wrong_dX_is_refused_on_every_stream(lib):
+    inp = make_head_case(HeadCase("wrong_dX", 8, 64, 256, 2, 351))
+    lp, kd = head(lib, inp, lib.LoraTokenLogProbs), head(lib, inp, lib.LoraDistill)
+    x = dev_bf16(inp["X"])
+    ids, t, dl, dlp = up(inp, "ids", "teacher", "dloss", "dlogprob")
+    o, d = lp.forward(x, ids), kd.forward(x, ids, t)
+    torch.cuda.synchronize()
+    for stream in (None, torch.cuda.Stream()):
+        for dX in (torch.empty_like(x, device="cpu"), torch.empty_like(x)[:4], x.float(), "dX"):
+            with pytest.raises(ValueError):
+                lp.backward(x, ids, o, dlp, dX=dX, stream=stream)
+            with pytest.raises(ValueError):
+                kd.backward(x, ids, t, d, dl, dX=dX, stream=stream)
